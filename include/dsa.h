@@ -366,6 +366,56 @@ dsa_status_t dsa_sparse_attn_decode_groups(const void *q, const void *k_cache, c
                                            float *lse, void *ws, size_t ws_bytes, dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------------ */
+/* The K/V cache in 8 bits: half the bytes of the bf16 cache for every page kept and every region
+ * gathered.  The pages give no format for it ([P3 §三] counts K/V at 2 bytes); this library's:
+ *   kv_cache    e4m3 [n_pages][4][8][2][8][192]  page, group, region of the page, K|V, token, dim
+ *   kv_scale    fp32 [n_pages][4][8][2]          one scale for every 8-token block, group and tensor
+ *   block_table int32 [n_req][max_pages]         as for the bf16 cache
+ * value = e4m3(code) * scale.  K and V of a region lie side by side (3 KiB: one load gathers
+ * both).  kv_cache is 16-byte aligned, kv_scale 8-byte aligned; max_pages < 2^31 / 64.
+ *
+ * dsa_kv_append_quant: quantises token i's K and V rows (new_k, new_v bf16 [n][4][192]) into row
+ * q_pos[i] % 64 of page block_table[b*max_pages + q_pos[i]/64], b = q_req[i] (q_req NULL: b = i).
+ * A block's scale is the smallest power of two s in [2^-126, 2^120] with max|x| <= 448 s (0 for
+ * zeros), a code is e4m3_RNE_satfinite(x / s).  Neighbouring list entries in one region of one
+ * request are a run and have ascending positions; a region has at most one run per call.  Below
+ * the first row of its run a block keeps its rows: its scale becomes the larger of the old one
+ * and the run's, and codes of a smaller scale are rounded again for it (exact for powers of two,
+ * but for e4m3 subnormals).  Rows behind the run keep their bytes, but not their values where the
+ * scale changes: a ring therefore holds the window and a region more (9 pages for 512 tokens), and
+ * a token is appended again after a rollback before it is attended.  Infinities saturate and
+ * take their block's scale to 2^120; NaN stays NaN and leaves the scale to the other values.  A
+ * q_req outside [0, n_req), a position that is negative or beyond the block table, a page
+ * outside [0, n_pages) and an entry that does not ascend in its run are skipped and flag
+ * DSA_ERR_DEVICE. */
+dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_pages, const int32_t *block_table,
+                                 int max_pages, int n_req, const int32_t *q_req, const int32_t *q_pos, int n,
+                                 const void *new_k, const void *new_v, dsa_stream_t stream);
+
+/* dsa_sparse_attn_decode_quant, dsa_sparse_attn_prefill_quant, dsa_window_attn_quant: the attention
+ * of dsa_sparse_attn_decode, dsa_sparse_attn_prefill and dsa_window_attn over this cache, with
+ * their arguments, results and errors (nq <= 2^24, out 8-byte aligned; a query at a negative
+ * position attends nothing: out = 0, lse = -inf).  Scales are finite and >= 0, powers of two or not.
+ * Scores and sums are fp32; q enters the products as two e4m3 terms (off by at most 2^-18 of the
+ * head's largest element), the softmax weights as fp16.  Tokens outside a query's T may hold any
+ * bytes, NaN codes among them.  The results do not depend on the other queries of the call.  No
+ * workspace. */
+dsa_status_t dsa_sparse_attn_decode_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
+                                          int64_t n_pages, const int32_t *block_table, int max_pages,
+                                          const int32_t *q_pos, int batch, const int32_t *sel_idx,
+                                          const int32_t *sel_count, int k, void *out, float *lse,
+                                          dsa_stream_t stream);
+dsa_status_t dsa_sparse_attn_prefill_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
+                                           int64_t n_pages, const int32_t *block_table, int max_pages, int n_req,
+                                           const int32_t *q_req, const int32_t *q_pos, int nq,
+                                           const int32_t *sel_idx, const int32_t *sel_count, int k, void *out,
+                                           float *lse, dsa_stream_t stream);
+dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale, int64_t n_pages,
+                                   const int32_t *block_table, int max_pages, int n_req, const int32_t *q_req,
+                                   const int32_t *q_pos, int nq, int window, void *out, float *lse,
+                                   dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
 /* Self-test of the failure detection (no counterpart in the pages).  Every mbarrier wait in
  * this library's kernels is bounded (2^31 SM cycles, about a second); a wait that runs out
  * sets the timeout bit of the per-device error word and lets its kernel return, so a stuck

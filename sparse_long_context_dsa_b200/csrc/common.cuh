@@ -27,6 +27,8 @@ enum : unsigned {
     kErrAttnIndex = 1u << 3,       // selected region / page out of range
     kErrWaitTimeout = 1u << 4,     // a bounded mbarrier wait gave up
     kErrTopkInternal = 1u << 5,    // selection bookkeeping inconsistent
+    kErrAppendOrder = 1u << 6,     // quantised append: a region's rows not in ascending order
+    kErrPages = 1u << 7,           // page fork / release / compact: an index, a count or no free page
 };
 
 __device__ unsigned int g_error_word;

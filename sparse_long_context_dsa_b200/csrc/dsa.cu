@@ -10,8 +10,10 @@
 #include <string>
 
 #include "../../include/dsa.h"
+#include "append_quant.cuh"
 #include "attention.cuh"
 #include "attention_cluster.cuh"
+#include "attention_quant.cuh"
 #include "attention_tc.cuh"
 #include "common.cuh"
 #include "compress.cuh"
@@ -684,6 +686,8 @@ dsa_status_t dsa_check_device(dsa_stream_t stream)
     if (word & dsa::kErrAttnIndex) msg += " attention region/page index out of range;";
     if (word & dsa::kErrWaitTimeout) msg += " bounded wait timed out;";
     if (word & dsa::kErrTopkInternal) msg += " top-k internal inconsistency;";
+    if (word & dsa::kErrAppendOrder) msg += " quantised append: positions of a region not ascending;";
+    if (word & dsa::kErrPages) msg += " pages: index or count out of range, or no free page;";
     return fail(DSA_ERR_DEVICE, msg);
 }
 
@@ -1152,6 +1156,122 @@ dsa_status_t dsa_sparse_attn_prefill(const void *q, const void *k_cache, const v
     DSA_REQUIRE(q_req != nullptr || nq == 0, "q_req must not be NULL");
     return attn_common(q, k_cache, v_cache, n_pages, block_table, max_pages, q_req, n_req, q_pos, nq, sel_idx,
                        sel_count, k, out, lse, ws, ws_bytes, stream);
+}
+
+namespace {
+// Checks that the calls on the quantised cache share.
+dsa_status_t quant_cache_args(const void *kv_cache, const float *kv_scale, int64_t n_pages,
+                              const int32_t *block_table, int max_pages)
+{
+    DSA_REQUIRE(kv_cache && kv_scale && block_table, "NULL pointer");
+    DSA_REQUIRE(aligned(kv_cache, 16) && aligned(kv_scale, 8), "kv_cache must be 16-byte, kv_scale 8-byte aligned");
+    return DSA_OK;
+}
+
+dsa_status_t quant_cache_sizes(int64_t n_pages, int max_pages)
+{
+    DSA_REQUIRE(n_pages >= 1 && n_pages <= (INT32_MAX / (dsa::kG * dsa::kPage)), "n_pages out of range");
+    DSA_REQUIRE(max_pages >= 1 && max_pages <= INT32_MAX / dsa::kPage, "max_pages out of [1, 2^31 / 64)");
+    return DSA_OK;
+}
+
+// window == 0: attention over the selection; window > 0: over each query's last `window` tokens.
+dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const float *kv_scale, int64_t n_pages,
+                               const int32_t *block_table, int max_pages, int n_req, const int32_t *q_req,
+                               const int32_t *q_pos, int nq, const int32_t *sel_idx, const int32_t *sel_count, int k,
+                               int window, void *out, float *lse, dsa_stream_t stream)
+{
+    DSA_REQUIRE(nq >= 0 && nq <= (1 << 24), "nq out of [0, 2^24]");
+    DSA_REQUIRE(window > 0 || (k >= 1 && k <= DSA_MAX_TOPK), "k out of [1, DSA_MAX_TOPK]");
+    dsa_status_t st = quant_cache_sizes(n_pages, max_pages);
+    if (st != DSA_OK) return st;
+    if (nq == 0) return DSA_OK;
+    DSA_REQUIRE(n_req >= 1, "n_req must be >= 1");
+    DSA_REQUIRE(q && q_pos && out && (window > 0 || (sel_idx && sel_count)), "NULL pointer");
+    if ((st = quant_cache_args(kv_cache, kv_scale, n_pages, block_table, max_pages)) != DSA_OK) return st;
+    DSA_REQUIRE(aligned(q, 16) && aligned(out, 8), "q must be 16-byte, out 8-byte aligned");
+    DSA_REACHABLE({q, "q"}, {kv_cache, "kv_cache"}, {kv_scale, "kv_scale"}, {block_table, "block_table"},
+                  {q_req, "q_req"}, {q_pos, "q_pos"}, {sel_idx, "sel_idx"}, {sel_count, "sel_count"}, {out, "out"},
+                  {lse, "lse"});
+    int sms = 0;
+    if ((st = device_info(sms)) != DSA_OK) return st;
+    dsa::attnq::Params p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.cache = kv_cache;
+    p.scale = kv_scale;
+    p.block_table = block_table;
+    p.q_req = q_req;
+    p.q_pos = q_pos;
+    p.sel_idx = sel_idx;
+    p.sel_count = sel_count;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.n_pages = n_pages;
+    p.max_pages = max_pages;
+    p.n_req = n_req;
+    p.nq = nq;
+    p.k = k;
+    p.window = window;
+    p.scale_log2 = dsa::attnq::kLog2e / sqrtf((float)dsa::kD);
+    return launch_k("sparse_attn_quant_kernel", dsa::attnq::sparse_attn_quant_kernel, dim3((unsigned)nq * dsa::kG),
+                    dim3(dsa::attnq::kThreads), 0, stream, 0, p);
+}
+}  // namespace
+
+dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_pages, const int32_t *block_table,
+                                 int max_pages, int n_req, const int32_t *q_req, const int32_t *q_pos, int n,
+                                 const void *new_k, const void *new_v, dsa_stream_t stream)
+{
+    DSA_REQUIRE(n >= 0, "n must be >= 0");
+    dsa_status_t st = quant_cache_sizes(n_pages, max_pages);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    DSA_REQUIRE(q_req == nullptr || n_req >= 1, "n_req must be >= 1");
+    DSA_REQUIRE(q_pos && new_k && new_v, "NULL pointer");
+    if ((st = quant_cache_args(kv_cache, kv_scale, n_pages, block_table, max_pages)) != DSA_OK) return st;
+    DSA_REQUIRE(aligned(new_k, 16) && aligned(new_v, 16), "new rows must be 16-byte aligned");
+    DSA_REACHABLE({kv_cache, "kv_cache"}, {kv_scale, "kv_scale"}, {block_table, "block_table"}, {q_req, "q_req"},
+                  {q_pos, "q_pos"}, {new_k, "new_k"}, {new_v, "new_v"});
+    int sms = 0;
+    if ((st = device_info(sms)) != DSA_OK) return st;
+    const int rows = q_req ? n_req : n;
+    const __nv_bfloat16 *nk = static_cast<const __nv_bfloat16 *>(new_k), *nv = static_cast<const __nv_bfloat16 *>(new_v);
+    // one list entry per CTA while that fills the GPU less than twice over (a decode step's runs
+    // are single tokens, and 8 of them in one CTA would wait for one another), else 8
+    if (n <= 2 * 8 * sms)
+        return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<1>, dim3((unsigned)n), dim3(256), 0,
+                        stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n, nk, nv);
+    return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<8>, dim3((unsigned)((n + 7) / 8)),
+                    dim3(256), 0, stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n,
+                    nk, nv);
+}
+
+dsa_status_t dsa_sparse_attn_decode_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
+                                          int64_t n_pages, const int32_t *block_table, int max_pages,
+                                          const int32_t *q_pos, int batch, const int32_t *sel_idx,
+                                          const int32_t *sel_count, int k, void *out, float *lse, dsa_stream_t stream)
+{
+    return attn_quant_common(q, kv_cache, kv_scale, n_pages, block_table, max_pages, batch, nullptr, q_pos, batch,
+                             sel_idx, sel_count, k, 0, out, lse, stream);
+}
+
+dsa_status_t dsa_sparse_attn_prefill_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
+                                           int64_t n_pages, const int32_t *block_table, int max_pages, int n_req,
+                                           const int32_t *q_req, const int32_t *q_pos, int nq, const int32_t *sel_idx,
+                                           const int32_t *sel_count, int k, void *out, float *lse, dsa_stream_t stream)
+{
+    DSA_REQUIRE(q_req != nullptr || nq == 0, "q_req must not be NULL");
+    return attn_quant_common(q, kv_cache, kv_scale, n_pages, block_table, max_pages, n_req, q_req, q_pos, nq, sel_idx,
+                             sel_count, k, 0, out, lse, stream);
+}
+
+dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale, int64_t n_pages,
+                                   const int32_t *block_table, int max_pages, int n_req, const int32_t *q_req,
+                                   const int32_t *q_pos, int nq, int window, void *out, float *lse, dsa_stream_t stream)
+{
+    DSA_REQUIRE(window >= 1 && window <= (1 << 20), "window out of [1, 2^20]");
+    return attn_quant_common(q, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req ? n_req : nq, q_req, q_pos,
+                             nq, nullptr, nullptr, 1, window, out, lse, stream);
 }
 
 dsa_status_t dsa_selftest_wait_timeout(int64_t limit_cycles, dsa_stream_t stream)

@@ -79,6 +79,15 @@ _SIG = {
     "dsa_window_attn_workspace_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int]),
     "dsa_indexer_frontend": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP, _I32P, _VP, _VP, _F32P,
                                             _VP]),
+    "dsa_kv_append_quant": (ctypes.c_int, [_U8P, _F32P, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int, _I32P,
+                                           _I32P, ctypes.c_int, _VP, _VP, _VP]),
+    "dsa_sparse_attn_decode_quant": (ctypes.c_int, [_VP, _U8P, _F32P, ctypes.c_int64, _I32P, ctypes.c_int, _I32P,
+                                                    ctypes.c_int, _I32P, _I32P, ctypes.c_int, _VP, _F32P, _VP]),
+    "dsa_sparse_attn_prefill_quant": (ctypes.c_int, [_VP, _U8P, _F32P, ctypes.c_int64, _I32P, ctypes.c_int,
+                                                     ctypes.c_int, _I32P, _I32P, ctypes.c_int, _I32P, _I32P,
+                                                     ctypes.c_int, _VP, _F32P, _VP]),
+    "dsa_window_attn_quant": (ctypes.c_int, [_VP, _U8P, _F32P, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int,
+                                             _I32P, _I32P, ctypes.c_int, ctypes.c_int, _VP, _F32P, _VP]),
     "dsa_window_attn": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int, _I32P,
                                        _I32P, ctypes.c_int, ctypes.c_int, _VP, _F32P, _VP, ctypes.c_size_t, _VP]),
     "dsa_window_decode": (ctypes.c_int, [_VP, _VP, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int, _I32P, _I32P,
@@ -467,6 +476,99 @@ def window_decode(q, k_cache, v_cache, block_table, q_pos, new_k, new_v, window=
     _check(lib().dsa_window_decode(_p(k_cache), _p(v_cache), k_cache.shape[0], _p(block_table), block_table.shape[1],
                                    block_table.shape[0], _p(q_req), _p(q_pos), nq, _p(new_k), _p(new_v), _p(q),
                                    int(window), _p(out), _p(lse), _p(ws), nbytes, _stream()))
+    return out
+
+
+QUANT_BLOCK = (PAGE // REGION, 2, REGION, D)      # a (page, group) of the 8-bit cache: region, K|V, token, dim
+
+
+def _quant_cache_args(kv_cache, kv_scale, block_table):
+    _need(kv_cache, torch.uint8, name="kv_cache")
+    if kv_cache.dim() != 6 or tuple(kv_cache.shape[1:]) != (G,) + QUANT_BLOCK:
+        raise ValueError("kv_cache must be [n_pages][4][8][2][8][192]")
+    _need(kv_scale, torch.float32, (kv_cache.shape[0], G, PAGE // REGION, 2), "kv_scale")
+    _need(block_table, torch.int32, name="block_table")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_req][max_pages]")
+
+
+def quant_cache(n_pages, device="cuda"):
+    """An empty 8-bit K/V cache: (kv_cache uint8 [n_pages][4][8][2][8][192] of e4m3 codes, kv_scale
+    fp32 [n_pages][4][8][2]); page, group, region of the page, K|V, token, dim."""
+    return (torch.zeros((n_pages, G) + QUANT_BLOCK, dtype=torch.uint8, device=device),
+            torch.zeros((n_pages, G, PAGE // REGION, 2), dtype=torch.float32, device=device))
+
+
+def kv_append_quant(kv_cache, kv_scale, block_table, q_pos, new_k, new_v, q_req=None):
+    """dsa_kv_append_quant: token i's K and V rows (new_k, new_v bf16 [n][4][192]) quantised into the
+    8-bit cache at position q_pos[i] of request q_req[i] (or i).  Tokens of one region are
+    neighbours in the list, in ascending order."""
+    _quant_cache_args(kv_cache, kv_scale, block_table)
+    n = q_pos.shape[0]
+    _need(q_pos, torch.int32, (n,), "q_pos")
+    _need(new_k, torch.bfloat16, (n, G, D), "new_k")
+    _need(new_v, torch.bfloat16, (n, G, D), "new_v")
+    if q_req is not None:
+        _need(q_req, torch.int32, (n,), "q_req")
+    elif n > block_table.shape[0]:
+        raise ValueError("without q_req token i is request i's: block_table needs a row for each")
+    _check(lib().dsa_kv_append_quant(_p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
+                                     block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), n, _p(new_k),
+                                     _p(new_v), _stream()))
+
+
+def _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse):
+    nq = q.shape[0]
+    _need(q, torch.bfloat16, (nq, HQ, D), "q")
+    _quant_cache_args(kv_cache, kv_scale, block_table)
+    _need(q_pos, torch.int32, (nq,), "q_pos")
+    if q_req is not None:
+        _need(q_req, torch.int32, (nq,), "q_req")
+    elif nq > block_table.shape[0]:
+        raise ValueError("without q_req query i is request i's: block_table needs a row for each")
+    if out is None:
+        out = torch.empty((nq, HQ, D), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, (nq, HQ, D), "out")
+    if lse is not None:
+        _need(lse, torch.float32, (nq, HQ), "lse")
+    return nq, out
+
+
+def _selection_args(nq, sel_idx, sel_count):
+    _need(sel_idx, torch.int32, name="sel_idx")
+    k = sel_idx.shape[-1]
+    _need(sel_idx, torch.int32, (nq, G, k), "sel_idx")
+    _need(sel_count, torch.int32, (nq, G), "sel_count")
+    return k
+
+
+def sparse_attn_decode_quant(q, kv_cache, kv_scale, block_table, q_pos, sel_idx, sel_count, out=None, lse=None):
+    """sparse_attn_decode over the 8-bit cache: one query per request.  Returns out bf16 [B][64][192]."""
+    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, None, out, lse)
+    k = _selection_args(nq, sel_idx, sel_count)
+    _check(lib().dsa_sparse_attn_decode_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
+                                              block_table.shape[1], _p(q_pos), nq, _p(sel_idx), _p(sel_count), k,
+                                              _p(out), _p(lse), _stream()))
+    return out
+
+
+def sparse_attn_prefill_quant(q, kv_cache, kv_scale, block_table, q_req, q_pos, sel_idx, sel_count, out=None,
+                              lse=None):
+    """sparse_attn_prefill over the 8-bit cache: queries of several requests.  Returns out."""
+    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse)
+    k = _selection_args(nq, sel_idx, sel_count)
+    _check(lib().dsa_sparse_attn_prefill_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
+                                               block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), nq,
+                                               _p(sel_idx), _p(sel_count), k, _p(out), _p(lse), _stream()))
+    return out
+
+
+def window_attn_quant(q, kv_cache, kv_scale, block_table, q_pos, window=512, q_req=None, out=None, lse=None):
+    """window_attn over the 8-bit cache.  Returns out bf16 [nq][64][192]."""
+    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse)
+    _check(lib().dsa_window_attn_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
+                                       block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), nq,
+                                       int(window), _p(out), _p(lse), _stream()))
     return out
 
 
