@@ -1,8 +1,12 @@
 // Sparse and window GQA over the 8-bit paged cache (layout and scales: append_quant.cuh).
 //
 // A row is (query, KV group): 16 query heads over the tokens of its regions (the selection, or
-// the window's regions), t <= p and inside the window.  One CTA of 4 warps per row streams the
-// regions in tiles of 8 (64 tokens):
+// the window's regions), t <= p and inside the window.  A cluster of S CTAs (S = 1, 2, .. 16:
+// more while there are few rows) shares a row, each a contiguous part of its regions, in tiles of
+// 8 regions (64 tokens):
+//  * a producer warp resolves the regions (sel_idx -> block_table -> block, scales; a region's
+//    lookups are spread over the tiles before it) and loads each with one TMA box (K and V rows
+//    lie side by side: 3 KiB) into a ring of kStages tiles; 4 warps compute:
 //  * S = q K^T on e4m3 tensor cores (mma.sync m16n8k32, fp32 accumulate) straight from the
 //    codes; a head's q is split into two e4m3 terms, q / 2^e = hi + lo, which is exact for
 //    elements above 2^-10 of the head's largest and off by at most 2^-18 of it below.  Warp w
@@ -13,7 +17,11 @@
 //    token within 2^-24 of the largest contribution is lost); l sums the unrounded fp32 P.
 //  * O += P' V with V's codes converted to fp16 (exact) on mma.sync m16n8k16, fp32 accumulate;
 //    warp w owns output dims [48w, 48w + 48), so no warp merges another's O.
-//  * out = O / l * 2^(M - m), lse = ln 2 (m + log2 l); an empty row gives 0 and -inf.
+//    One barrier per tile: the references move (and a second one is taken) only when some token
+//    passes one by more than 2^8; until then P' stays below 2^8.
+//  * out = O / l * 2^(M - m), lse = ln 2 (m + log2 l); an empty row gives 0 and -inf.  With S > 1
+//    the CTA's (O, m, M, l) of head h goes to CTA h mod S as one bulk copy that completes on that
+//    CTA's inbox barrier, and CTA r merges heads r, r + S, ... and writes them.
 // Rows of V that no token attends (behind the query, before the window, regions that are not
 // there) are zeroed in shared memory: their P' is 0, but 0 * NaN is not.
 #pragma once
@@ -27,7 +35,8 @@ namespace dsa {
 namespace attnq {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kThreads = 32 * (kWarps + 1);                      // and the producer warp
+constexpr int kStages = 3;
 constexpr int kTileRegions = 8;                                  // 64 tokens
 constexpr int kRegBytes = quant::kRegionBytesQ;                  // 3 KiB: K rows, then V rows
 constexpr int kTileBytes = kTileRegions * kRegBytes;
@@ -35,11 +44,25 @@ constexpr int kQRow = kD + 16;                                   // q code rows,
 constexpr int kPRow = 2 * 64 + 16;                               // P' tile row (bytes), padded
 constexpr float kSlack = 8.0f;                                   // log2 units a reference may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kInRow = kD + 4;                                   // inbox row: O, m, M, l, pad
+
+// Dynamic shared memory, after the ring (which begins on a 1,024-byte boundary).
+struct Smem {
+    float inbox[kHeadsPerGroup * kInRow];                        // S > 1: (source CTA, its head slot)
+    uint8_t qcodes[2][16 * kQRow];                               // hi, lo
+    uint8_t ptile[2][16 * kPRow];
+    float qscale[16];
+    float mx[kWarps][16][2];
+    float l[kWarps][16];
+    uint64_t full[kStages], empty[kStages], inbox_bar;
+    int region[kStages][kTileRegions];                           // -1: none
+    float2 scale[kStages][kTileRegions];                         // of K and V
+};
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
 
 struct Params {
     const __nv_bfloat16 *q;      // [nq][64][192]
-    const uint8_t *cache;
-    const float *scale;
+    const float2 *scale;         // [pages][4][8]: K's and V's
     const int32_t *block_table;
     const int32_t *q_req;        // nullptr: identity
     const int32_t *q_pos;
@@ -51,6 +74,7 @@ struct Params {
     int max_pages, n_req, nq, k;
     int window;                  // 0: the selection
     float scale_log2;            // log2(e) / sqrt(192)
+    int splits;                  // CTAs (the cluster) per row: 1, 2, 4, 8 or 16
 };
 
 // Byte offset of (row, col) in a region's [16 rows: 8 K, 8 V][192 B]: 64-byte lines with the
@@ -86,21 +110,53 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Params p)
+// Barrier of the 4 computing warps; _or: true when `pred` holds for one of their threads.
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool warps_sync_or(bool pred)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)pred)
+        : "memory");
+    return r != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+    sparse_attn_quant_kernel(const __grid_constant__ CUtensorMap tmap, const Params p)
 {
     pdl_trigger();   // the next kernel may launch; it waits for this one itself
-    pdl_wait();      // the previous kernel's results are visible from here on
-    __shared__ __align__(128) uint8_t tile[kTileBytes];
-    __shared__ __align__(16) uint8_t qcodes[2][16 * kQRow];      // hi, lo
-    __shared__ float qscale[16];
-    __shared__ __align__(16) uint8_t ptile[2][16 * kPRow];
-    __shared__ float mx_sh[kWarps][16][2];
-    __shared__ float l_sh[kWarps][16];
-    __shared__ int r_sh[kTileRegions];                           // region (-1: none)
-    __shared__ float ks_sh[kTileRegions], vs_sh[kTileRegions];
-
+    if (threadIdx.x == 0) prefetch_tensormap(&tmap);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem &sm = *reinterpret_cast<Smem *>(ring + kStages * kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
-    const int g = (int)(blockIdx.x / (unsigned)p.nq), qi = (int)(blockIdx.x % (unsigned)p.nq);
+    const int S = p.splits;
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.full[i], 2);                           // the loads are announced; the scales are there
+            mbar_init(&sm.empty[i], kWarps);
+        }
+        mbar_init(&sm.inbox_bar, 1);
+        mbar_arrive_expect_tx(&sm.inbox_bar, (unsigned)(kHeadsPerGroup * kInRow * 4));
+        fence_mbar_init();
+    }
+    // every CTA's inbox barrier is set up before any CTA copies into it
+    if (S > 1) {
+        __syncwarp();
+        cluster_arrive_relaxed();
+    }
+    pdl_wait();      // the previous kernel's results are visible from here on
+
+    // rows in group-major order: the CTAs resident together gather from one group's share
+    const unsigned rid_row = blockIdx.x / (unsigned)S;
+    const int rank = (int)(blockIdx.x % (unsigned)S);
+    const int g = (int)(rid_row / (unsigned)p.nq), qi = (int)(rid_row % (unsigned)p.nq);
     const int b = p.q_req ? p.q_req[qi] : qi;
     const int pos = p.q_pos[qi];
     const int row = qi * kG + g;
@@ -116,32 +172,101 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
         cnt = min(max(raw, 0), p.k);
         if (tid == 0 && cnt != raw) set_error(kErrAttnIndex);
     }
+    // this CTA's regions: [j_lo, j_lo + n_reg) of the row's
+    const int per = (cnt + S - 1) / S;
+    const int j_lo = min(cnt, rank * per), n_reg = min(cnt - j_lo, per);
+    const int n_tiles = (n_reg + kTileRegions - 1) / kTileRegions;
+    __syncthreads();                                             // the barriers are set up
+
+    if (warp == kWarps) {
+        // ---- producer: lane l holds region 32 n + l of the CTA (n: the batch of 4 tiles)
+        auto region_of = [&](int j) -> int {
+            if (j >= n_reg) return -1;
+            return p.window > 0 ? (t_lo >> 3) + j_lo + j : p.sel_idx[(int64_t)row * p.k + j_lo + j];
+        };
+        auto page_of = [&](int j, int r) -> int {
+            if (j >= n_reg) return -1;
+            if (r >= 0 && r / 8 < p.max_pages) {
+                const int page = p.block_table[(int64_t)b * p.max_pages + r / 8];
+                if (page >= 0 && page < p.n_pages) return page;
+            }
+            set_error(kErrAttnIndex);
+            return -1;
+        };
+        int r = region_of(lane), page = page_of(lane, r);
+        int block = page < 0 ? -1 : (page * kG + g) * quant::kRegionsPerPage + r % 8;
+        float2 sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
+        int r_n = -1, block_n = -1;                              // the next batch's
+        float2 sc_n = make_float2(0.0f, 0.0f);
+        bool ok = true;
+        for (int ti = 0; ti < n_tiles; ++ti) {
+            const int st = ti % kStages, sub = ti & 3;
+            if (ti >= kStages) ok = __all_sync(0xffffffffu, mbar_wait_sleep(&sm.empty[st], (unsigned)(ti / kStages - 1) & 1u));
+            if (!ok) break;
+            const bool mine = (lane >> 3) == sub;
+            const unsigned there = __ballot_sync(0xffffffffu, mine && block >= 0);
+            if (lane == 0) {
+                if (there) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(__popc(there) * kRegBytes));
+                else mbar_arrive(&sm.full[st]);
+            }
+            __syncwarp();
+            if (mine) {
+                if (block >= 0)
+                    tma_load_3d(ring + st * kTileBytes + (lane & 7) * kRegBytes, &tmap, 0, 0, block * 16, &sm.full[st]);
+                sm.region[st][lane & 7] = block < 0 ? -1 : r;
+                sm.scale[st][lane & 7] = sc;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[st]);
+            // the next batch's lookups, one dependent load per tile of this batch
+            const int jn = (ti & ~3) * kTileRegions + 32 + lane;
+            if (sub == 0) {
+                r_n = region_of(jn);
+            } else if (sub == 1) {
+                const int pg = page_of(jn, r_n);
+                block_n = pg < 0 ? -1 : (pg * kG + g) * quant::kRegionsPerPage + r_n % 8;
+            } else if (sub == 2) {
+                sc_n = block_n < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block_n);
+            } else {
+                r = r_n;
+                block = block_n;
+                sc = sc_n;
+            }
+        }
+        if (S > 1) cluster_wait();
+        return;
+    }
 
     // q of head h, 2^-e q = hi + lo in e4m3 (warp w: heads 4w .. 4w + 3; lane: 6 elements)
-    for (int h = 4 * warp; h < 4 * warp + 4; ++h) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + ((int64_t)qi * kHQ + g * kHeadsPerGroup + h) * kD);
-        float v[6], a = 0.0f;
+    {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            p.q + ((int64_t)qi * kHQ + g * kHeadsPerGroup + 4 * warp) * kD) + lane;
+        uint32_t w[4][3];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            const uint32_t w = __ldg(src + lane + 32 * j);
-            v[2 * j] = bf16_lo(w);
-            v[2 * j + 1] = bf16_hi(w);
-            a = fmaxf(a, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
-        }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-        if (lane == 0) qscale[h] = s * p.scale_log2;
+            for (int j = 0; j < 3; ++j) w[i][j] = __ldg(src + i * (kD / 2) + 32 * j);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            const float x = v[2 * j] * inv, y = v[2 * j + 1] * inv;
-            const uint32_t hi = cvt_e4m3x2(x, y);
-            const uint32_t lo = cvt_e4m3x2(x - e4m3_to_f32(hi), y - e4m3_to_f32(hi >> 8));
-            *reinterpret_cast<uint16_t *>(qcodes[0] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t *>(qcodes[1] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)lo;
+        for (int i = 0; i < 4; ++i) {
+            const int h = 4 * warp + i;
+            float a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[i][j])), fabsf(bf16_hi(w[i][j]))));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            if (lane == 0) sm.qscale[h] = s * p.scale_log2;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const float x = bf16_lo(w[i][j]) * inv, y = bf16_hi(w[i][j]) * inv;
+                const uint32_t hi = cvt_e4m3x2(x, y);
+                const uint32_t lo = cvt_e4m3x2(x - e4m3_to_f32(hi), y - e4m3_to_f32(hi >> 8));
+                *reinterpret_cast<uint16_t *>(sm.qcodes[0] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)hi;
+                *reinterpret_cast<uint16_t *>(sm.qcodes[1] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)lo;
+            }
         }
     }
-    __syncthreads();
+    warps_sync();
     // A fragments of q: rows gq, gq + 8; k = 32 ks + 4t .. + 3 and + 16
     uint32_t qa[2][6][4];
 #pragma unroll
@@ -150,9 +275,9 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
         for (int ks = 0; ks < 6; ++ks)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                qa[s][ks][i] = *reinterpret_cast<const uint32_t *>(qcodes[s] + (gq + 8 * (i & 1)) * kQRow + 32 * ks +
+                qa[s][ks][i] = *reinterpret_cast<const uint32_t *>(sm.qcodes[s] + (gq + 8 * (i & 1)) * kQRow + 32 * ks +
                                                                   16 * (i >> 1) + 4 * t);
-    const float qf[2] = {qscale[gq], qscale[gq + 8]};
+    const float qf[2] = {sm.qscale[gq], sm.qscale[gq + 8]};
 
     float o[3][2][4];                                            // 16-dim block, even / odd dims
 #pragma unroll
@@ -162,52 +287,14 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
     float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY};      // references (rows gq, gq + 8)
     float c[2] = {0.0f, 0.0f};                                   // 2^(m - M)
     float l[2] = {0.0f, 0.0f};                                   // this thread's part of the sum
+    bool landed = true;
 
-    const int n_tiles = (cnt + kTileRegions - 1) / kTileRegions;
     for (int ti = 0; ti < n_tiles; ++ti) {
-        const int j0 = ti * kTileRegions, nr = min(kTileRegions, cnt - j0);
-        __syncthreads();                                         // the previous tile is done with
-        if (tid < kTileRegions) {
-            int r = -1;
-            float ks = 0.0f, vs = 0.0f;
-            int64_t rid = 0;
-            if (tid < nr) {
-                r = p.window > 0 ? (t_lo >> 3) + j0 + tid : p.sel_idx[(int64_t)row * p.k + j0 + tid];
-                const int64_t page = (r < 0 || r / 8 >= p.max_pages) ? -1 : p.block_table[(int64_t)b * p.max_pages + r / 8];
-                if (page < 0 || page >= p.n_pages) {
-                    set_error(kErrAttnIndex);
-                    r = -1;
-                } else {
-                    rid = (page * kG + g) * quant::kRegionsPerPage + r % 8;
-                    ks = p.scale[2 * rid];
-                    vs = p.scale[2 * rid + 1];
-                }
-            }
-            r_sh[tid] = r;
-            ks_sh[tid] = ks;
-            vs_sh[tid] = vs;
-            // the region's address travels through the tile's first bytes of its slot
-            *reinterpret_cast<int64_t *>(tile + tid * kRegBytes) = rid;
-        }
-        __syncthreads();
-        int64_t rid[kTileRegions];
-#pragma unroll
-        for (int j = 0; j < kTileRegions; ++j) rid[j] = *reinterpret_cast<const int64_t *>(tile + j * kRegBytes);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kTileRegions; ++j) {
-            const bool there = r_sh[j] >= 0;
-            for (int i = tid; i < kRegBytes / 16; i += kThreads) {
-                const int rr = i / (kD / 16), cc = i % (kD / 16);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                // rows of V that no token attends stay zero
-                const int tok = 8 * r_sh[j] + (rr & 7);
-                if (there && (rr < 8 || (tok <= pos && tok >= t_lo)))
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.cache + rid[j] * kRegBytes) + i);
-                *reinterpret_cast<uint4 *>(tile + j * kRegBytes + swz(rr, cc * 16)) = v;
-            }
-        }
-        __syncthreads();
+        const int st = ti % kStages;
+        // a wait that gives up leaves the error flag and garbage; the others are then short, and
+        // every barrier is still met
+        if (!mbar_wait(&sm.full[st], (unsigned)(ti / kStages) & 1u, landed ? kWaitLimitCycles : 1ll << 24)) landed = false;
+        uint8_t *tile = ring + st * kTileBytes;
 
         // ---- S of regions 2w, 2w + 1
         float s[2][4];
@@ -215,6 +302,20 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
             const int j = 2 * warp + nt;
+            const int r = sm.region[st][j];
+            const int u0 = r < 0 ? 8 : max(0, t_lo - 8 * r), u1 = r < 0 ? 8 : min(8, pos - 8 * r + 1);  // rows attended
+            if (u0 > 0 || u1 < 8) {
+                // V rows that no token attends: zero, whatever they hold
+                for (int i = lane; i < 8 * (kD / 16); i += 32) {
+                    const int rr = i / (kD / 16);
+                    if (rr < u0 || rr >= u1)
+                        *reinterpret_cast<uint4 *>(tile + j * kRegBytes + swz(8 + rr, (i % (kD / 16)) * 16)) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();                             // before the ring's next load of these bytes
+            }
+            s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = -INFINITY;
+            if (u0 >= u1) continue;
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             const uint32_t base = smem_u32(tile + j * kRegBytes);
 #pragma unroll
@@ -227,14 +328,13 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
                     mma_e4m3_16832(acc, qa[x][2 * kb + 1], b2, b3);
                 }
             }
-            const int r = r_sh[j];
-            const float ks = ks_sh[j], lv = log2f(vs_sh[j]);
+            const float2 sc = sm.scale[st][j];
+            const float lv = log2f(sc.y);
             float mr[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int tok = 8 * r + 2 * t + (e & 1);
-                const bool ok = r >= 0 && tok <= pos && tok >= t_lo;
-                s[nt][e] = ok ? acc[e] * (qf[e >> 1] * ks) : -INFINITY;
+                const int u = 2 * t + (e & 1);
+                if (u >= u0 && u < u1) s[nt][e] = acc[e] * (qf[e >> 1] * sc.x);
                 mr[e >> 1] = fmaxf(mr[e >> 1], s[nt][e]);
             }
 #pragma unroll
@@ -246,7 +346,26 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
         // ---- move the references where a token passes them by more than the slack
         const bool grow = mxs[0] > m[0] + kSlack || mxs[1] > m[1] + kSlack || mxv[0] > M[0] + kSlack ||
                           mxv[1] > M[1] + kSlack;
-        if (__syncthreads_or(grow)) {
+        auto write_p = [&]() {
+            const float mref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+            uint8_t *pt = sm.ptile[ti & 1];
+            float add[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const float vs = sm.scale[st][2 * warp + nt].y;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = exp2f(s[nt][2 * h] - mref[h]), p1 = exp2f(s[nt][2 * h + 1] - mref[h]);
+                    add[h] += p0 + p1;
+                    const float f = fminf(vs * c[h], 8.5070592e37f);               // 2^126
+                    *reinterpret_cast<uint32_t *>(pt + (gq + 8 * h) * kPRow + 2 * (16 * warp + 8 * nt + 2 * t)) =
+                        pack_f16x2(p0 * f, p1 * f);
+                }
+            }
+            return make_float2(add[0], add[1]);
+        };
+        float2 add = write_p();                                  // right unless some reference moves
+        if (warps_sync_or(grow)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 mxs[h] = fmaxf(mxs[h], __shfl_xor_sync(0xffffffffu, mxs[h], 1));
@@ -254,18 +373,18 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
                 mxv[h] = fmaxf(mxv[h], __shfl_xor_sync(0xffffffffu, mxv[h], 1));
                 mxv[h] = fmaxf(mxv[h], __shfl_xor_sync(0xffffffffu, mxv[h], 2));
                 if (t == 0) {
-                    mx_sh[warp][gq + 8 * h][0] = mxs[h];
-                    mx_sh[warp][gq + 8 * h][1] = mxv[h];
+                    sm.mx[warp][gq + 8 * h][0] = mxs[h];
+                    sm.mx[warp][gq + 8 * h][1] = mxv[h];
                 }
             }
-            __syncthreads();
+            warps_sync();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float a = m[h], d = M[h];
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    a = fmaxf(a, mx_sh[w][gq + 8 * h][0]);
-                    d = fmaxf(d, mx_sh[w][gq + 8 * h][1]);
+                    a = fmaxf(a, sm.mx[w][gq + 8 * h][0]);
+                    d = fmaxf(d, sm.mx[w][gq + 8 * h][1]);
                 }
                 const float al = m[h] == a ? 1.0f : exp2f(m[h] - a), ao = M[h] == d ? 1.0f : exp2f(M[h] - d);
                 l[h] *= al;
@@ -280,30 +399,20 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
                 M[h] = d;
                 c[h] = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
             }
+            add = write_p();
+            warps_sync();
         }
-        // ---- P' of regions 2w, 2w + 1
-        const float mref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-        uint8_t *pt = ptile[ti & 1];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const float vs = vs_sh[2 * warp + nt];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float p0 = exp2f(s[nt][2 * h] - mref[h]), p1 = exp2f(s[nt][2 * h + 1] - mref[h]);
-                l[h] += p0 + p1;
-                const float f = fminf(vs * c[h], 8.5070592e37f);                   // 2^126
-                *reinterpret_cast<uint32_t *>(pt + (gq + 8 * h) * kPRow + 2 * (16 * warp + 8 * nt + 2 * t)) =
-                    pack_f16x2(p0 * f, p1 * f);
-            }
-        }
-        __syncthreads();
+        l[0] += add.x;
+        l[1] += add.y;
         // ---- O[:, 48w .. 48w + 47] += P' V, two k-steps (4 regions) at a time
+        const uint32_t pt = smem_u32(sm.ptile[ti & 1]);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
+            if (kk == 1 && n_reg - ti * kTileRegions <= 4) break;
             uint32_t pa[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                ldmatrix_x4(smem_u32(pt) + (lane & 15) * kPRow + 64 * kk + 32 * x + 16 * (lane >> 4), pa[x][0], pa[x][1],
+                ldmatrix_x4(pt + (lane & 15) * kPRow + 64 * kk + 32 * x + 16 * (lane >> 4), pa[x][0], pa[x][1],
                             pa[x][2], pa[x][3]);
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
@@ -315,38 +424,91 @@ __global__ void __launch_bounds__(kThreads) sparse_attn_quant_kernel(const Param
                     // (token 2t: dims d, d + 1)(token 2t + 1: dims d, d + 1) -> pairs of tokens per dim
                     const uint32_t a = __byte_perm(v[2 * x], 0, 0x3120), bb = __byte_perm(v[2 * x + 1], 0, 0x3120);
                     mma_f16_16816(o[j][0], pa[x], e4m3x2_to_f16x2((uint16_t)a), e4m3x2_to_f16x2((uint16_t)bb));
-                    mma_f16_16816(o[j][1], pa[x], e4m3x2_to_f16x2((uint16_t)(a >> 16)), e4m3x2_to_f16x2((uint16_t)(bb >> 16)));
+                    mma_f16_16816(o[j][1], pa[x], e4m3x2_to_f16x2((uint16_t)(a >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)(bb >> 16)));
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);
     }
 
-    // ---- the row's sums, then the outputs of this warp's dims
+    // ---- the CTA's sums
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (t == 0) l_sh[warp][gq + 8 * h] = l[h];
+        if (t == 0) sm.l[warp][gq + 8 * h] = l[h];
     }
-    __syncthreads();
+    warps_sync();
+    const int64_t head0 = (int64_t)qi * kHQ + g * kHeadsPerGroup;
+    float L[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        L[h] = (sm.l[0][gq + 8 * h] + sm.l[1][gq + 8 * h]) + (sm.l[2][gq + 8 * h] + sm.l[3][gq + 8 * h]);
+    if (S == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
+            const float f = L[h] > 0.0f ? (M[h] > -INFINITY ? exp2f(M[h] - m[h]) / L[h] : 0.0f) : L[h];
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                *reinterpret_cast<uint2 *>(p.out + (head0 + gq + 8 * h) * kD + 48 * warp + 16 * j + 4 * t) =
+                    make_uint2(pack_bf16x2(o[j][0][2 * h] * f, o[j][1][2 * h] * f),
+                               pack_bf16x2(o[j][0][2 * h + 1] * f, o[j][1][2 * h + 1] * f));
+            if (p.lse && warp == 0 && t == 0)
+                p.lse[head0 + gq + 8 * h] = L[h] == 0.0f ? -INFINITY : (m[h] + log2f(L[h])) * 0.69314718055994531f;
+        }
+        return;
+    }
+    // ---- (O, m, M, l) of head h to CTA h % S, inbox row (rank, h / S); staged in the ring, whose
+    // loads have all been waited for
+    float *stage = reinterpret_cast<float *>(ring);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int hr = gq + 8 * h;
-        const float L = (l_sh[0][hr] + l_sh[1][hr]) + (l_sh[2][hr] + l_sh[3][hr]);
-        const int64_t head = (int64_t)qi * kHQ + g * kHeadsPerGroup + hr;
-        const float f = L > 0.0f && M[h] > -INFINITY ? exp2f(M[h] - m[h]) / L : 0.0f;
-        // NaN stays NaN: L is then NaN too, and no comparison holds
-        const float z = L == L ? f : L;
+        float *in = stage + (gq + 8 * h) * kInRow;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            const int d = 48 * warp + 16 * j + 4 * t;
-            const uint2 v = make_uint2(pack_bf16x2(o[j][0][2 * h] * z, o[j][1][2 * h] * z),
-                                       pack_bf16x2(o[j][0][2 * h + 1] * z, o[j][1][2 * h + 1] * z));
-            *reinterpret_cast<uint2 *>(p.out + head * kD + d) = v;
-        }
-        if (p.lse && warp == 0 && t == 0)
-            p.lse[head] = L == 0.0f ? -INFINITY : (m[h] + log2f(L)) * 0.69314718055994531f;
+        for (int j = 0; j < 3; ++j)
+            *reinterpret_cast<float4 *>(in + 48 * warp + 16 * j + 4 * t) =
+                make_float4(o[j][0][2 * h], o[j][1][2 * h], o[j][0][2 * h + 1], o[j][1][2 * h + 1]);
+        if (warp == 0 && t == 0) *reinterpret_cast<float4 *>(in + kD) = make_float4(m[h], M[h], L[h], 0.0f);
     }
+    fence_proxy_async();                                         // the rows, to the copy engine
+    __syncwarp();
+    cluster_wait();
+    warps_sync();
+    const int per_cta = kHeadsPerGroup / S;                      // heads this CTA merges
+    if (warp == 0 && lane < kHeadsPerGroup) {
+        bulk_copy_to_cta(sm.inbox + (rank * per_cta + lane / S) * kInRow, stage + lane * kInRow,
+                         (unsigned)(kInRow * 4), &sm.inbox_bar, (unsigned)(lane % S));
+        bulk_commit();
+    }
+    const bool inbox_ok = mbar_wait(&sm.inbox_bar, 0u);          // false: error set
+    for (int e = tid; inbox_ok && e < per_cta * (kD / 2); e += 32 * kWarps) {
+        const int j = e / (kD / 2), d = 2 * (e % (kD / 2));
+        float mm = -INFINITY, MM = -INFINITY;
+        for (int cc = 0; cc < S; ++cc) {
+            const float *in = sm.inbox + (cc * per_cta + j) * kInRow;
+            mm = fmaxf(mm, in[kD]);
+            MM = fmaxf(MM, in[kD + 1]);
+        }
+        const float mref = mm == -INFINITY ? 0.0f : mm, Mref = MM == -INFINITY ? 0.0f : MM;
+        float Ls = 0.0f, x = 0.0f, y = 0.0f;
+        for (int cc = 0; cc < S; ++cc) {
+            const float *in = sm.inbox + (cc * per_cta + j) * kInRow;
+            const float2 v = *reinterpret_cast<const float2 *>(in + d);
+            const float wt = exp2f(in[kD + 1] - Mref);
+            Ls += exp2f(in[kD] - mref) * in[kD + 2];
+            x += wt * v.x;
+            y += wt * v.y;
+        }
+        const float f = Ls > 0.0f ? (MM > -INFINITY ? exp2f(MM - mm) / Ls : 0.0f) : Ls;
+        const int64_t head = head0 + rank + S * j;
+        *reinterpret_cast<uint32_t *>(p.out + head * kD + d) = pack_bf16x2(x * f, y * f);
+        if (p.lse && d == 0) p.lse[head] = Ls == 0.0f ? -INFINITY : (mm + log2f(Ls)) * 0.69314718055994531f;
+    }
+    // this CTA's copies have read their rows before its shared memory goes away
+    if (warp == 0 && lane < kHeadsPerGroup) bulk_wait_read_all();
 }
 
 }  // namespace attnq

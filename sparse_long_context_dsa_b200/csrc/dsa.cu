@@ -1170,8 +1170,34 @@ dsa_status_t quant_cache_args(const void *kv_cache, const float *kv_scale, int64
 
 dsa_status_t quant_cache_sizes(int64_t n_pages, int max_pages)
 {
-    DSA_REQUIRE(n_pages >= 1 && n_pages <= (INT32_MAX / (dsa::kG * dsa::kPage)), "n_pages out of range");
+    DSA_REQUIRE(n_pages >= 1 && n_pages <= (INT32_MAX / (2 * dsa::kG * dsa::kPage)), "n_pages out of range");
     DSA_REQUIRE(max_pages >= 1 && max_pages <= INT32_MAX / dsa::kPage, "max_pages out of [1, 2^31 / 64)");
+    return DSA_OK;
+}
+
+// CTAs of the quantised attention that the device holds at once; sets the kernel's attributes on
+// the device's first call.
+dsa_status_t attn_quant_resident(int &ctas, int sms)
+{
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static int per_sm[kMaxDevices] = {};
+    int dev = 0;
+    DSA_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return fail(DSA_ERR_UNSUPPORTED, "device ordinal out of range");
+    std::lock_guard<std::mutex> lock(mu);
+    if (per_sm[dev] == 0) {
+        const auto fn = dsa::attnq::sparse_attn_quant_kernel;
+        DSA_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnq::kSmemBytes),
+                 "cudaFuncSetAttribute(sparse_attn_quant_kernel)");
+        DSA_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                 "cudaFuncSetAttribute(sparse_attn_quant_kernel)");
+        int n = 0;
+        DSA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, dsa::attnq::kThreads, dsa::attnq::kSmemBytes),
+                 "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+        per_sm[dev] = std::max(1, n);
+    }
+    ctas = per_sm[dev] * sms;
     return DSA_OK;
 }
 
@@ -1195,10 +1221,21 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
                   {lse, "lse"});
     int sms = 0;
     if ((st = device_info(sms)) != DSA_OK) return st;
+    int resident = 0;
+    if ((st = attn_quant_resident(resident, sms)) != DSA_OK) return st;
+    CUtensorMap map;
+    {
+        // codes as [n_pages * 4 * 8 regions * 16 rows][3][64]: one region (8 K rows, 8 V rows) = box {64, 3, 16}
+        const cuuint64_t dims[3] = {64, 3, (cuuint64_t)n_pages * dsa::kG * (dsa::kPage / dsa::kRegion) * 16};
+        const cuuint64_t strides[2] = {64, (cuuint64_t)dsa::kD};
+        const cuuint32_t box[3] = {64, 3, 16};
+        if ((st = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv_cache, dims, strides, box,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_64B)) != DSA_OK)
+            return st;
+    }
     dsa::attnq::Params p{};
     p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.cache = kv_cache;
-    p.scale = kv_scale;
+    p.scale = reinterpret_cast<const float2 *>(kv_scale);
     p.block_table = block_table;
     p.q_req = q_req;
     p.q_pos = q_pos;
@@ -1213,8 +1250,15 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     p.k = k;
     p.window = window;
     p.scale_log2 = dsa::attnq::kLog2e / sqrtf((float)dsa::kD);
-    return launch_k("sparse_attn_quant_kernel", dsa::attnq::sparse_attn_quant_kernel, dim3((unsigned)nq * dsa::kG),
-                    dim3(dsa::attnq::kThreads), 0, stream, 0, p);
+    // CTAs per row: as many as fit the GPU at once, while each keeps half a tile of regions
+    const int64_t rows = (int64_t)nq * dsa::kG;
+    const int most = window > 0 ? window_regions(window) : k;
+    p.splits = 1;
+    while (p.splits < 16 && rows * p.splits * 2 <= resident && most >= 2 * p.splits * (dsa::attnq::kTileRegions / 2))
+        p.splits *= 2;
+    return launch_k("sparse_attn_quant_kernel", dsa::attnq::sparse_attn_quant_kernel,
+                    dim3((unsigned)(rows * p.splits)), dim3(dsa::attnq::kThreads), dsa::attnq::kSmemBytes, stream,
+                    p.splits > 1 ? (unsigned)p.splits : 0u, map, p);
 }
 }  // namespace
 
