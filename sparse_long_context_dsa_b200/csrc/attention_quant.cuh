@@ -7,10 +7,12 @@
 //  * a producer warp resolves the regions (sel_idx -> block_table -> block, scales; a region's
 //    lookups are spread over the tiles before it) and loads each with one TMA box (K and V rows
 //    lie side by side: 3 KiB) into a ring of kStages tiles; 4 warps compute:
-//  * S = q K^T on e4m3 tensor cores (mma.sync m16n8k32, fp32 accumulate) straight from the
-//    codes; a head's q is split into two e4m3 terms, q / 2^e = hi + lo, which is exact for
-//    elements above 2^-10 of the head's largest and off by at most 2^-18 of it below.  Warp w
-//    takes regions 2w and 2w + 1 of the tile.  The K scale multiplies the finished dot product.
+//  * S = q K^T on mma.sync m16n8k16 fp16 (fp32 accumulate).  K's codes convert to fp16 exactly, and
+//    so does 2^-e q (e per head, the largest element in [2^14, 2^15)) but for elements below
+//    2^-32 of the head's largest, off by 2^-40 of it at most.  (The e4m3 mma.sync of this GPU runs
+//    as two fp16 ones and their conversions: 21 cycles a k-step of 32 for q in two e4m3 terms
+//    against 8 for each k-step of 16 here.)  Warp w takes regions 2w and 2w + 1 of the tile.  The K
+//    scale multiplies the finished dot product.
 //  * softmax in fp32, log2 units, with a running reference m per head for the sum l.  The P that
 //    meets V carries the V scale, so it has a reference of its own: P' = 2^(s - m) * sV * 2^(m -
 //    M), M the running maximum of s + log2 sV.  P' is rounded to fp16 (2^-12 relative, and no
@@ -36,27 +38,29 @@ namespace attnq {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);                      // and the producer warp
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+constexpr int kCtasPerSm = 3;
 constexpr int kTileRegions = 8;                                  // 64 tokens
 constexpr int kRegBytes = quant::kRegionBytesQ;                  // 3 KiB: K rows, then V rows
 constexpr int kTileBytes = kTileRegions * kRegBytes;
-constexpr int kQRow = kD + 16;                                   // q code rows, padded against bank conflicts
+constexpr int kQRow = 2 * kD + 16;                               // fp16 q rows (bytes), padded against bank conflicts
 constexpr int kPRow = 2 * 64 + 16;                               // P' tile row (bytes), padded
-constexpr float kSlack = 8.0f;                                   // log2 units a reference may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kInRow = kD + 4;                                   // inbox row: O, m, M, l, pad
 
 // Dynamic shared memory, after the ring (which begins on a 1,024-byte boundary).
 struct Smem {
-    float inbox[kHeadsPerGroup * kInRow];                        // S > 1: (source CTA, its head slot)
-    uint8_t qcodes[2][16 * kQRow];                               // hi, lo
+    union {
+        float inbox[kHeadsPerGroup * kInRow];                    // S > 1: (source CTA, its head slot)
+        uint8_t q[16 * kQRow];                                   // before the cluster's first barrier
+    };
     uint8_t ptile[2][16 * kPRow];
     float qscale[16];
     float mx[kWarps][16][2];
     float l[kWarps][16];
     uint64_t full[kStages], empty[kStages], inbox_bar;
     int region[kStages][kTileRegions];                           // -1: none
-    float2 scale[kStages][kTileRegions];                         // of K and V
+    float4 scale[kStages][kTileRegions];                         // K's, V's, log2 of V's
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
 
@@ -94,6 +98,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v)
     return r;
 }
 
+// 2^x to 2 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -108,6 +120,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b)
+{
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Either of two fp16 weights (>= 0, or NaN) above 2^8.
+__device__ __forceinline__ bool any_above_256(uint32_t v)
+{
+    return __hgt2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0x5C00))) != 0u;
 }
 
 // Barrier of the 4 computing warps; _or: true when `pred` holds for one of their threads.
@@ -126,7 +150,7 @@ __device__ __forceinline__ bool warps_sync_or(bool pred)
     return r != 0;
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     sparse_attn_quant_kernel(const __grid_constant__ CUtensorMap tmap, const Params p)
 {
     pdl_trigger();   // the next kernel may launch; it waits for this one itself
@@ -145,11 +169,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(&sm.inbox_bar, 1);
         mbar_arrive_expect_tx(&sm.inbox_bar, (unsigned)(kHeadsPerGroup * kInRow * 4));
         fence_mbar_init();
-    }
-    // every CTA's inbox barrier is set up before any CTA copies into it
-    if (S > 1) {
-        __syncwarp();
-        cluster_arrive_relaxed();
     }
     pdl_wait();      // the previous kernel's results are visible from here on
 
@@ -179,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();                                             // the barriers are set up
 
     if (warp == kWarps) {
+        if (S > 1) cluster_arrive();
         // ---- producer: lane l holds region 32 n + l of the CTA (n: the batch of 4 tiles)
         auto region_of = [&](int j) -> int {
             if (j >= n_reg) return -1;
@@ -214,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (block >= 0)
                     tma_load_3d(ring + st * kTileBytes + (lane & 7) * kRegBytes, &tmap, 0, 0, block * 16, &sm.full[st]);
                 sm.region[st][lane & 7] = block < 0 ? -1 : r;
-                sm.scale[st][lane & 7] = sc;
+                sm.scale[st][lane & 7] = make_float4(sc.x, sc.y, log2f(sc.y), 0.0f);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.full[st]);
@@ -233,11 +253,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 sc = sc_n;
             }
         }
+        __syncwarp();
         if (S > 1) cluster_wait();
         return;
     }
 
-    // q of head h, 2^-e q = hi + lo in e4m3 (warp w: heads 4w .. 4w + 3; lane: 6 elements)
+    // 2^-e q of head h in fp16 (warp w: heads 4w .. 4w + 3; lane: 6 elements)
     {
         const uint32_t *src = reinterpret_cast<const uint32_t *>(
             p.q + ((int64_t)qi * kHQ + g * kHeadsPerGroup + 4 * warp) * kD) + lane;
@@ -254,30 +275,33 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int j = 0; j < 3; ++j) a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[i][j])), fabsf(bf16_hi(w[i][j]))));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            // block_scale puts the largest element in [224, 448]; 2^6 more, into [2^13, 2^15)
             const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-            if (lane == 0) sm.qscale[h] = s * p.scale_log2;
+            if (lane == 0) sm.qscale[h] = s * (p.scale_log2 * 0.015625f);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const float x = bf16_lo(w[i][j]) * inv, y = bf16_hi(w[i][j]) * inv;
-                const uint32_t hi = cvt_e4m3x2(x, y);
-                const uint32_t lo = cvt_e4m3x2(x - e4m3_to_f32(hi), y - e4m3_to_f32(hi >> 8));
-                *reinterpret_cast<uint16_t *>(sm.qcodes[0] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)hi;
-                *reinterpret_cast<uint16_t *>(sm.qcodes[1] + h * kQRow + 2 * (lane + 32 * j)) = (uint16_t)lo;
-            }
+            for (int j = 0; j < 3; ++j)
+                *reinterpret_cast<uint32_t *>(sm.q + h * kQRow + 4 * (lane + 32 * j)) =
+                    pack_f16x2(bf16_lo(w[i][j]) * inv * 64.0f, bf16_hi(w[i][j]) * inv * 64.0f);
         }
     }
     warps_sync();
-    // A fragments of q: rows gq, gq + 8; k = 32 ks + 4t .. + 3 and + 16
-    uint32_t qa[2][6][4];
+    // A fragments of q, rows gq and gq + 8.  A k-step is a 16-byte chunk of K's codes: a thread's 4
+    // codes 4t .. 4t + 3 of it are k = 2t, 2t + 1, 2t + 8, 2t + 9, for q as for K.
+    uint32_t qa[12][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int ks = 0; ks < 12; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < 6; ++ks)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                qa[s][ks][i] = *reinterpret_cast<const uint32_t *>(sm.qcodes[s] + (gq + 8 * (i & 1)) * kQRow + 32 * ks +
-                                                                  16 * (i >> 1) + 4 * t);
+        for (int h = 0; h < 2; ++h) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(sm.q + (gq + 8 * h) * kQRow + 32 * ks + 8 * t);
+            qa[ks][h] = v.x;
+            qa[ks][2 + h] = v.y;
+        }
     const float qf[2] = {sm.qscale[gq], sm.qscale[gq + 8]};
+    if (S > 1) {
+        // every CTA's inbox barrier is set up, and its q read, before any CTA copies into its inbox
+        __syncwarp();
+        cluster_arrive();
+    }
 
     float o[3][2][4];                                            // 16-dim block, even / odd dims
 #pragma unroll
@@ -287,7 +311,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY};      // references (rows gq, gq + 8)
     float c[2] = {0.0f, 0.0f};                                   // 2^(m - M)
     float l[2] = {0.0f, 0.0f};                                   // this thread's part of the sum
+    float mref[2] = {0.0f, 0.0f};                                // m, or 0 for -inf
     bool landed = true;
+    // the lane's ldmatrix offsets: K chunks 4 kb .. + 3 of row lane % 8 (region 2 warp), V chunk
+    // 3 warp + j (row lane % 8 of region lane / 8), P' rows
+    uint32_t koff[3], voff[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        koff[j] = smem_u32(ring) + 2 * warp * kRegBytes + swz(lane & 7, j * 64 + 16 * (lane >> 3));
+        voff[j] = smem_u32(ring) + (lane >> 3) * kRegBytes + swz(8 + (lane & 7), 48 * warp + 16 * j);
+    }
+    const uint32_t poff = smem_u32(sm.ptile[0]) + (lane & 15) * kPRow + 16 * (lane >> 4);
+    uint8_t *pw = sm.ptile[0] + gq * kPRow + 2 * (16 * warp + 2 * t);
 
     for (int ti = 0; ti < n_tiles; ++ti) {
         const int st = ti % kStages;
@@ -298,83 +333,75 @@ __global__ void __launch_bounds__(kThreads, 2)
 
         // ---- S of regions 2w, 2w + 1
         float s[2][4];
-        float mxs[2] = {-INFINITY, -INFINITY}, mxv[2] = {-INFINITY, -INFINITY};
+        float4 sc[2];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
             const int j = 2 * warp + nt;
             const int r = sm.region[st][j];
-            const int u0 = r < 0 ? 8 : max(0, t_lo - 8 * r), u1 = r < 0 ? 8 : min(8, pos - 8 * r + 1);  // rows attended
-            if (u0 > 0 || u1 < 8) {
-                // V rows that no token attends: zero, whatever they hold
+            sc[nt] = sm.scale[st][j];
+            float acc[2][4] = {};                                // even and odd chunks: two chains
+#pragma unroll
+            for (int kb = 0; kb < 3; ++kb) {
+                uint32_t v[4];
+                ldmatrix_x4(koff[kb] + st * kTileBytes + nt * kRegBytes, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mma_f16_16816(acc[x & 1], qa[4 * kb + x], e4m3x2_to_f16x2((uint16_t)v[x]),
+                                  e4m3x2_to_f16x2((uint16_t)(v[x] >> 16)));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = (acc[0][e] + acc[1][e]) * (qf[e >> 1] * sc[nt].x);
+            if (r < 0 || 8 * r < t_lo || 8 * r + 7 > pos) {
+                // some rows are attended by no token (the own region, the window's first, none there):
+                // their scores are -inf and their V rows zero, whatever they hold
+                const int u0 = r < 0 ? 8 : t_lo - 8 * r, u1 = pos - 8 * r;       // attended: u0 <= row <= u1
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int u = 2 * t + (e & 1);
+                    if (u < u0 || u > u1) s[nt][e] = -INFINITY;
+                }
                 for (int i = lane; i < 8 * (kD / 16); i += 32) {
                     const int rr = i / (kD / 16);
-                    if (rr < u0 || rr >= u1)
+                    if (rr < u0 || rr > u1)
                         *reinterpret_cast<uint4 *>(tile + j * kRegBytes + swz(8 + rr, (i % (kD / 16)) * 16)) =
                             make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();                             // before the ring's next load of these bytes
             }
-            s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = -INFINITY;
-            if (u0 >= u1) continue;
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const uint32_t base = smem_u32(tile + j * kRegBytes);
-#pragma unroll
-            for (int kb = 0; kb < 3; ++kb) {
-                uint32_t b0, b1, b2, b3;
-                ldmatrix_x4(base + swz(lane & 7, kb * 64 + 16 * (lane >> 3)), b0, b1, b2, b3);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mma_e4m3_16832(acc, qa[x][2 * kb], b0, b1);
-                    mma_e4m3_16832(acc, qa[x][2 * kb + 1], b2, b3);
-                }
-            }
-            const float2 sc = sm.scale[st][j];
-            const float lv = log2f(sc.y);
-            float mr[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int u = 2 * t + (e & 1);
-                if (u >= u0 && u < u1) s[nt][e] = acc[e] * (qf[e >> 1] * sc.x);
-                mr[e >> 1] = fmaxf(mr[e >> 1], s[nt][e]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mxs[h] = fmaxf(mxs[h], mr[h]);
-                mxv[h] = fmaxf(mxv[h], mr[h] + lv);
-            }
         }
-        // ---- move the references where a token passes them by more than the slack
-        const bool grow = mxs[0] > m[0] + kSlack || mxs[1] > m[1] + kSlack || mxv[0] > M[0] + kSlack ||
-                          mxv[1] > M[1] + kSlack;
-        auto write_p = [&]() {
-            const float mref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-            uint8_t *pt = sm.ptile[ti & 1];
-            float add[2] = {0.0f, 0.0f};
+        // ---- P' of regions 2w, 2w + 1, for the references as they are
+        uint32_t pp[2][2];
+        float add[2];
+        auto weights = [&]() {
+            add[0] = add[1] = 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const float vs = sm.scale[st][2 * warp + nt].y;
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float p0 = exp2f(s[nt][2 * h] - mref[h]), p1 = exp2f(s[nt][2 * h + 1] - mref[h]);
+                    const float p0 = ex2(s[nt][2 * h] - mref[h]), p1 = ex2(s[nt][2 * h + 1] - mref[h]);
                     add[h] += p0 + p1;
-                    const float f = fminf(vs * c[h], 8.5070592e37f);               // 2^126
-                    *reinterpret_cast<uint32_t *>(pt + (gq + 8 * h) * kPRow + 2 * (16 * warp + 8 * nt + 2 * t)) =
-                        pack_f16x2(p0 * f, p1 * f);
+                    const float f = fminf(sc[nt].y * c[h], 8.5070592e37f);         // 2^126
+                    pp[nt][h] = pack_f16x2(p0 * f, p1 * f);
+                    *reinterpret_cast<uint32_t *>(pw + (ti & 1) * (16 * kPRow) + 8 * h * kPRow + 16 * nt) = pp[nt][h];
                 }
-            }
-            return make_float2(add[0], add[1]);
         };
-        float2 add = write_p();                                  // right unless some reference moves
+        weights();
+        // a reference has to move when a weight passes 2^8 (a thread's four of l: 2^10), or when
+        // there is none yet; a NaN moves nothing
+        const uint32_t top = max_f16x2(max_f16x2(pp[0][0], pp[0][1]), max_f16x2(pp[1][0], pp[1][1]));
+        const bool grow = fmaxf(add[0], add[1]) > 1024.0f || any_above_256(top) || fminf(M[0], M[1]) == -INFINITY;
         if (warps_sync_or(grow)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                mxs[h] = fmaxf(mxs[h], __shfl_xor_sync(0xffffffffu, mxs[h], 1));
-                mxs[h] = fmaxf(mxs[h], __shfl_xor_sync(0xffffffffu, mxs[h], 2));
-                mxv[h] = fmaxf(mxv[h], __shfl_xor_sync(0xffffffffu, mxv[h], 1));
-                mxv[h] = fmaxf(mxv[h], __shfl_xor_sync(0xffffffffu, mxv[h], 2));
+                const float x = fmaxf(s[0][2 * h], s[0][2 * h + 1]), y = fmaxf(s[1][2 * h], s[1][2 * h + 1]);
+                float mxs = fmaxf(x, y), mxv = fmaxf(x + sc[0].z, y + sc[1].z);
+                mxs = fmaxf(mxs, __shfl_xor_sync(0xffffffffu, mxs, 1));
+                mxs = fmaxf(mxs, __shfl_xor_sync(0xffffffffu, mxs, 2));
+                mxv = fmaxf(mxv, __shfl_xor_sync(0xffffffffu, mxv, 1));
+                mxv = fmaxf(mxv, __shfl_xor_sync(0xffffffffu, mxv, 2));
                 if (t == 0) {
-                    sm.mx[warp][gq + 8 * h][0] = mxs[h];
-                    sm.mx[warp][gq + 8 * h][1] = mxv[h];
+                    sm.mx[warp][gq + 8 * h][0] = mxs;
+                    sm.mx[warp][gq + 8 * h][1] = mxv;
                 }
             }
             warps_sync();
@@ -397,28 +424,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 m[h] = a;
                 M[h] = d;
+                mref[h] = a == -INFINITY ? 0.0f : a;
                 c[h] = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
             }
-            add = write_p();
+            weights();
             warps_sync();
         }
-        l[0] += add.x;
-        l[1] += add.y;
+        l[0] += add[0];
+        l[1] += add[1];
         // ---- O[:, 48w .. 48w + 47] += P' V, two k-steps (4 regions) at a time
-        const uint32_t pt = smem_u32(sm.ptile[ti & 1]);
+        const uint32_t pt = poff + (ti & 1) * (16 * kPRow);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             if (kk == 1 && n_reg - ti * kTileRegions <= 4) break;
             uint32_t pa[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                ldmatrix_x4(pt + (lane & 15) * kPRow + 64 * kk + 32 * x + 16 * (lane >> 4), pa[x][0], pa[x][1],
-                            pa[x][2], pa[x][3]);
+                ldmatrix_x4(pt + 64 * kk + 32 * x, pa[x][0], pa[x][1], pa[x][2], pa[x][3]);
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
                 uint32_t v[4];
-                ldmatrix_x4_trans(smem_u32(tile + (4 * kk + (lane >> 3)) * kRegBytes) +
-                                      swz(8 + (lane & 7), 48 * warp + 16 * j), v[0], v[1], v[2], v[3]);
+                ldmatrix_x4_trans(voff[j] + st * kTileBytes + 4 * kk * kRegBytes, v[0], v[1], v[2], v[3]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     // (token 2t: dims d, d + 1)(token 2t + 1: dims d, d + 1) -> pairs of tokens per dim
