@@ -416,6 +416,54 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
                                    dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------------ */
+/* Pages shared between requests (no counterpart in the pages: what a serving runtime does with a
+ * paged cache, without a host synchronisation).  ref int32 [n_pages] counts the table entries that
+ * hold a page (0 or less: free); block_table int32 [n_req][max_pages], -1 where a request has no
+ * page.  Every call reads ref_in and table_in and leaves its result, whole, in ref_out and table_out;
+ * an output may be its input itself (in place) but not overlap it otherwise.  An allocation takes
+ * the lowest free pages, so results are functions of the arguments alone.  n <= 4096,
+ * max_pages < 2^31 / 64.  A pool is an array [n_pages] of pages of page_bytes (a multiple of 16,
+ * 16-byte aligned): the caches of every layer that share a block table, with their scales.
+ * `pools` is a host array, read during the call; pools must not overlap one another.
+ *
+ * dsa_pages_fork: for i = 0 .. n - 1, row child[i] becomes a request of the first length[i] tokens
+ *   of row parent[i]: it shares the full pages (their counts rise) and, for a partly filled last
+ *   page, holds a copy of it in a page of its own: the j-th free page, j the number of forks
+ *   before it that copy one.  Other entries of the row become -1 (whatever it held is not
+ *   released).  A child is no fork's parent and no other fork's child in the same call.
+ * dsa_pages_release: row req[i] is cut to its first keep[i] tokens (0: all given back): pages
+ *   behind them lose this holder, their entries become -1.
+ * dsa_pages_compact: the n_live live pages move to the places 0 .. n_live - 1: those behind, from
+ *   the last one down, go to the free places among them, from the first one up.  new_index int32
+ *   [n_pages]: the new place of every page, -1 for a free one; n_live int32 [1].  The table, the
+ *   counts and every pool's pages follow; what a page left behind holds is unspecified.
+ *
+ * Flagged with DSA_ERR_DEVICE: a row outside [0, n_req), a length outside the table, a negative
+ * keep, a clash of children or a request named twice (that entry of the call does nothing); an
+ * entry that names no page or a free one, and a fork with no free page left (that table entry
+ * becomes -1).  Workspaces: 256-byte aligned, dsa_pages_fork_workspace_size(n) and
+ * dsa_pages_compact_workspace_size(n_pages) bytes.  The summaries of a forked request lie where its
+ * sum_base says, not in pages: dsa_copy copies them, one call per group. */
+#define DSA_MAX_PAGE_POOLS 8
+typedef struct dsa_page_pool {
+    void *data;
+    int64_t page_bytes;
+} dsa_page_pool_t;
+size_t dsa_pages_fork_workspace_size(int n);
+dsa_status_t dsa_pages_fork(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                            int32_t *table_out, int max_pages, int n_req, const int32_t *parent,
+                            const int32_t *child, const int32_t *length, int n, const dsa_page_pool_t *pools,
+                            int n_pools, void *ws, size_t ws_bytes, dsa_stream_t stream);
+dsa_status_t dsa_pages_release(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                               int32_t *table_out, int max_pages, int n_req, const int32_t *req,
+                               const int32_t *keep, int n, dsa_stream_t stream);
+size_t dsa_pages_compact_workspace_size(int64_t n_pages);
+dsa_status_t dsa_pages_compact(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                               int32_t *table_out, int max_pages, int n_req, int32_t *new_index, int32_t *n_live,
+                               const dsa_page_pool_t *pools, int n_pools, void *ws, size_t ws_bytes,
+                               dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------ */
 /* Self-test of the failure detection (no counterpart in the pages).  Every mbarrier wait in
  * this library's kernels is bounded (2^31 SM cycles, about a second); a wait that runs out
  * sets the timeout bit of the per-device error word and lets its kernel return, so a stuck

@@ -21,6 +21,7 @@
 #include "frontend.cuh"
 #include "gemm_indexer.cuh"
 #include "indexer.cuh"
+#include "pages.cuh"
 #include "selftest.cuh"
 #include "topk.cuh"
 #include "topk_cluster.cuh"
@@ -648,6 +649,26 @@ dsa_status_t static_scratch(int dev, void **ptr)
     return DSA_OK;
 }
 
+// Runs `set` (a CUDA call) once on every device that the process uses, with that device current.
+struct PerDevice {
+    static constexpr int kMax = 64;
+    std::mutex mu;
+    bool done[kMax] = {};
+    template <typename F>
+    dsa_status_t once(F set)
+    {
+        int dev = 0;
+        DSA_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+        if (dev < 0 || dev >= kMax) return fail(DSA_ERR_UNSUPPORTED, "device ordinal out of range");
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev]) {
+            DSA_CUDA(set(), "kernel attributes");
+            done[dev] = true;
+        }
+        return DSA_OK;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -1175,30 +1196,14 @@ dsa_status_t quant_cache_sizes(int64_t n_pages, int max_pages)
     return DSA_OK;
 }
 
-// CTAs of the quantised attention that the device holds at once; sets the kernel's attributes on
-// the device's first call.
-dsa_status_t attn_quant_resident(int &ctas, int sms)
+dsa_status_t attn_quant_attributes()
 {
-    constexpr int kMaxDevices = 64;
-    static std::mutex mu;
-    static int per_sm[kMaxDevices] = {};
-    int dev = 0;
-    DSA_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-    if (dev < 0 || dev >= kMaxDevices) return fail(DSA_ERR_UNSUPPORTED, "device ordinal out of range");
-    std::lock_guard<std::mutex> lock(mu);
-    if (per_sm[dev] == 0) {
+    static PerDevice attr;
+    return attr.once([] {
         const auto fn = dsa::attnq::sparse_attn_quant_kernel;
-        DSA_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnq::kSmemBytes),
-                 "cudaFuncSetAttribute(sparse_attn_quant_kernel)");
-        DSA_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
-                 "cudaFuncSetAttribute(sparse_attn_quant_kernel)");
-        int n = 0;
-        DSA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, dsa::attnq::kThreads, dsa::attnq::kSmemBytes),
-                 "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-        per_sm[dev] = std::max(1, n);
-    }
-    ctas = per_sm[dev] * sms;
-    return DSA_OK;
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnq::kSmemBytes);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
 }
 
 // window == 0: attention over the selection; window > 0: over each query's last `window` tokens.
@@ -1221,8 +1226,8 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
                   {lse, "lse"});
     int sms = 0;
     if ((st = device_info(sms)) != DSA_OK) return st;
-    int resident = 0;
-    if ((st = attn_quant_resident(resident, sms)) != DSA_OK) return st;
+    if ((st = attn_quant_attributes()) != DSA_OK) return st;
+    const int resident = dsa::attnq::kCtasPerSm * sms;
     CUtensorMap map;
     {
         // codes as [n_pages * 4 * 8 regions * 16 rows][3][64]: one region (8 K rows, 8 V rows) = box {64, 3, 16}
@@ -1316,6 +1321,182 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
     DSA_REQUIRE(window >= 1 && window <= (1 << 20), "window out of [1, 2^20]");
     return attn_quant_common(q, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req ? n_req : nq, q_req, q_pos,
                              nq, nullptr, nullptr, 1, window, out, lse, stream);
+}
+
+// ---- pages: fork, release, compact
+namespace {
+constexpr int kMaxListed = 4096;      // forks or releases of one call (each looks at the others)
+
+dsa_status_t page_table_args(const int32_t *ref_in, const int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                             const int32_t *table_out, int max_pages, int n_req)
+{
+    DSA_REQUIRE(n_pages >= 1 && n_pages <= INT32_MAX, "n_pages out of range");
+    DSA_REQUIRE(max_pages >= 1 && max_pages <= INT32_MAX / dsa::kPage, "max_pages out of [1, 2^31 / 64)");
+    DSA_REQUIRE(n_req >= 1, "n_req must be >= 1");
+    DSA_REQUIRE(ref_in && ref_out && table_in && table_out, "NULL pointer");
+    DSA_REQUIRE(aligned(ref_in, 4) && aligned(ref_out, 4) && aligned(table_in, 4) && aligned(table_out, 4),
+                "misaligned pointer");
+    const auto overlap = [](const int32_t *a, const int32_t *b, int64_t n) { return a != b && a < b + n && b < a + n; };
+    DSA_REQUIRE(!overlap(ref_in, ref_out, n_pages) && !overlap(table_in, table_out, (int64_t)n_req * max_pages),
+                "an output may be its input itself, but not overlap it");
+    DSA_REACHABLE({ref_in, "ref_in"}, {ref_out, "ref_out"}, {table_in, "table_in"}, {table_out, "table_out"});
+    return DSA_OK;
+}
+
+dsa_status_t page_pools(const dsa_page_pool_t *pools, int n_pools, dsa::pages::Pools &out)
+{
+    DSA_REQUIRE(n_pools >= 0 && n_pools <= DSA_MAX_PAGE_POOLS, "n_pools out of [0, DSA_MAX_PAGE_POOLS]");
+    DSA_REQUIRE(n_pools == 0 || pools, "NULL pointer");
+    out = dsa::pages::Pools{};
+    out.n = n_pools;
+    for (int i = 0; i < n_pools; ++i) {
+        DSA_REQUIRE(pools[i].data, "NULL pointer");
+        DSA_REQUIRE(aligned(pools[i].data, 16) && pools[i].page_bytes >= 16 && pools[i].page_bytes % 16 == 0 &&
+                        pools[i].page_bytes <= (1ll << 32),
+                    "a pool must be 16-byte aligned, its page a multiple of 16 bytes and at most 2^32");
+        DSA_REACHABLE({pools[i].data, "pool"});
+        out.data[i] = static_cast<uint8_t *>(pools[i].data);
+        out.bytes[i] = pools[i].page_bytes;
+        out.first[i + 1] = out.first[i] + (int)((pools[i].page_bytes + dsa::pages::kSegment - 1) / dsa::pages::kSegment);
+    }
+    return DSA_OK;
+}
+
+// The cluster that scans n_pages counts (one CTA for every 4,096 of them, at most 16) and, behind
+// it, clusters that copy the inputs where the outputs are other arrays.
+dsa_status_t launch_page_scan(bool compact, const dsa::pages::Scan &a, int sms, dsa_stream_t stream)
+{
+    const auto fn = compact ? dsa::pages::scan_kernel<true> : dsa::pages::scan_kernel<false>;
+    static PerDevice attr;
+    dsa_status_t st = attr.once([] {
+        const cudaError_t e = cudaFuncSetAttribute(dsa::pages::scan_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(dsa::pages::scan_kernel<false>,
+                                                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (st != DSA_OK) return st;
+    const int64_t steps = (a.n_pages + dsa::pages::kPer - 1) / dsa::pages::kPer;
+    int size = 1;
+    while (size < 16 && size < steps) size *= 2;
+    const int64_t copies = (a.ref_out != a.ref_in ? a.n_pages : 0) + (a.table_out != a.table_in ? a.table_n : 0);
+    const int64_t want = (copies + 4 * dsa::pages::kScanThreads - 1) / (4 * dsa::pages::kScanThreads);
+    const int64_t clusters = 1 + std::min<int64_t>((want + size - 1) / size, sms / size);
+    return launch_k("page scan_kernel", fn, dim3((unsigned)(size * clusters)), dim3(dsa::pages::kScanThreads), 0, stream,
+                    (unsigned)size, a);
+}
+}  // namespace
+
+size_t dsa_pages_fork_workspace_size(int n)
+{
+    return n <= 0 ? 0 : round_up(((size_t)n + 1) * 4, 256);
+}
+
+dsa_status_t dsa_pages_fork(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                            int32_t *table_out, int max_pages, int n_req, const int32_t *parent, const int32_t *child,
+                            const int32_t *length, int n, const dsa_page_pool_t *pools, int n_pools, void *ws,
+                            size_t ws_bytes, dsa_stream_t stream)
+{
+    DSA_REQUIRE(n >= 0 && n <= kMaxListed, "n out of [0, 4096]");
+    dsa_status_t st = page_table_args(ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req);
+    if (st != DSA_OK) return st;
+    DSA_REQUIRE(n == 0 || (parent && child && length), "NULL pointer");
+    dsa::pages::Pools pp;
+    if ((st = page_pools(pools, n_pools, pp)) != DSA_OK) return st;
+    DSA_REACHABLE({parent, "parent"}, {child, "child"}, {length, "length"}, {ws, "ws"});
+    const size_t need = dsa_pages_fork_workspace_size(n);
+    if (n > 0 && (!ws || ws_bytes < need || !aligned(ws, 256)))
+        return fail(DSA_ERR_WORKSPACE, "fork workspace too small or not 256-byte aligned (need " + std::to_string(need) +
+                                           " bytes)");
+    int sms = 0;
+    if ((st = device_info(sms)) != DSA_OK) return st;
+    const int64_t table_n = (int64_t)n_req * max_pages;
+    if (n == 0) {
+        if (ref_out == ref_in && table_out == table_in) return DSA_OK;
+        return launch_k("copy_tables_kernel", dsa::pages::copy_tables_kernel, dim3((unsigned)sms), dim3(dsa::pages::kThreads),
+                        0, stream, 0, ref_in, ref_out, n_pages, table_in, table_out, table_n);
+    }
+    dsa::pages::Scan a{};
+    a.ref_in = ref_in;
+    a.ref_out = ref_out;
+    a.n_pages = n_pages;
+    a.table_in = table_in;
+    a.table_out = table_out;
+    a.table_n = table_n;
+    a.n_live = static_cast<int32_t *>(ws);
+    a.list = a.n_live + 1;
+    a.want = n;
+    if ((st = launch_page_scan(false, a, sms, stream)) != DSA_OK) return st;
+    const int segs = pp.first[pp.n];
+    const int ctas = std::max(1, std::min(segs, 4 * sms / n));       // of a fork: they share its copied page
+    return launch_k("fork_kernel", dsa::pages::fork_kernel, dim3((unsigned)ctas, (unsigned)n), dim3(dsa::pages::kThreads), 0,
+                    stream, 0, ref_out, n_pages, table_in, table_out, max_pages, n_req, parent, child, length, n,
+                    static_cast<const int32_t *>(a.list), static_cast<const int32_t *>(a.n_live), pp);
+}
+
+dsa_status_t dsa_pages_release(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                               int32_t *table_out, int max_pages, int n_req, const int32_t *req, const int32_t *keep,
+                               int n, dsa_stream_t stream)
+{
+    DSA_REQUIRE(n >= 0 && n <= kMaxListed, "n out of [0, 4096]");
+    dsa_status_t st = page_table_args(ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req);
+    if (st != DSA_OK) return st;
+    DSA_REQUIRE(n == 0 || (req && keep), "NULL pointer");
+    DSA_REACHABLE({req, "req"}, {keep, "keep"});
+    int sms = 0;
+    if ((st = device_info(sms)) != DSA_OK) return st;
+    const int64_t table_n = (int64_t)n_req * max_pages;
+    if (ref_out != ref_in || table_out != table_in) {
+        const int64_t want = (n_pages + table_n + 4 * dsa::pages::kThreads - 1) / (4 * dsa::pages::kThreads);
+        if ((st = launch_k("copy_tables_kernel", dsa::pages::copy_tables_kernel,
+                           dim3((unsigned)std::min<int64_t>(want, 4 * sms)), dim3(dsa::pages::kThreads), 0, stream, 0,
+                           ref_in, ref_out, n_pages, table_in, table_out, table_n)) != DSA_OK)
+            return st;
+    }
+    if (n == 0) return DSA_OK;
+    const int ctas = std::max(1, std::min((max_pages + dsa::pages::kThreads - 1) / dsa::pages::kThreads, 8 * sms / n));
+    return launch_k("release_kernel", dsa::pages::release_kernel, dim3((unsigned)ctas, (unsigned)n),
+                    dim3(dsa::pages::kThreads), 0, stream, 0, ref_out, n_pages, table_out, max_pages, n_req, req, keep, n);
+}
+
+size_t dsa_pages_compact_workspace_size(int64_t n_pages)
+{
+    return n_pages < 1 ? 0 : 256 + 3 * round_up((size_t)n_pages * 4, 256);
+}
+
+dsa_status_t dsa_pages_compact(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
+                               int32_t *table_out, int max_pages, int n_req, int32_t *new_index, int32_t *n_live,
+                               const dsa_page_pool_t *pools, int n_pools, void *ws, size_t ws_bytes,
+                               dsa_stream_t stream)
+{
+    dsa_status_t st = page_table_args(ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req);
+    if (st != DSA_OK) return st;
+    DSA_REQUIRE(new_index && n_live, "NULL pointer");
+    DSA_REACHABLE({new_index, "new_index"}, {n_live, "n_live"}, {ws, "ws"});
+    dsa::pages::Pools pp;
+    if ((st = page_pools(pools, n_pools, pp)) != DSA_OK) return st;
+    const size_t need = dsa_pages_compact_workspace_size(n_pages);
+    if (!ws || ws_bytes < need || !aligned(ws, 256))
+        return fail(DSA_ERR_WORKSPACE, "compact workspace too small or not 256-byte aligned (need " +
+                                           std::to_string(need) + " bytes)");
+    int sms = 0;
+    if ((st = device_info(sms)) != DSA_OK) return st;
+    const size_t row = round_up((size_t)n_pages * 4, 256);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    dsa::pages::Scan a{};
+    a.ref_in = ref_in;
+    a.ref_out = ref_out;
+    a.n_pages = n_pages;
+    a.table_in = a.table_out = table_out;                            // move_kernel writes the table
+    a.n_moves = reinterpret_cast<int32_t *>(w);
+    a.list = reinterpret_cast<int32_t *>(w + 256);
+    a.movers = reinterpret_cast<int32_t *>(w + 256 + row);
+    a.place = reinterpret_cast<int32_t *>(w + 256 + 2 * row);
+    a.new_index = new_index;
+    a.n_live = n_live;
+    if ((st = launch_page_scan(true, a, sms, stream)) != DSA_OK) return st;
+    return launch_k("move_kernel", dsa::pages::move_kernel, dim3((unsigned)(8 * sms)), dim3(dsa::pages::kThreads), 0, stream,
+                    0, ref_in, ref_out, n_pages, table_in, table_out, (int64_t)n_req * max_pages,
+                    static_cast<const int32_t *>(a.list), static_cast<const int32_t *>(a.movers),
+                    static_cast<const int32_t *>(a.place), new_index, static_cast<const int32_t *>(a.n_moves), pp);
 }
 
 dsa_status_t dsa_selftest_wait_timeout(int64_t limit_cycles, dsa_stream_t stream)

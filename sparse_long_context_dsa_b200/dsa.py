@@ -88,6 +88,14 @@ _SIG = {
                                                      ctypes.c_int, _VP, _F32P, _VP]),
     "dsa_window_attn_quant": (ctypes.c_int, [_VP, _U8P, _F32P, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int,
                                              _I32P, _I32P, ctypes.c_int, ctypes.c_int, _VP, _F32P, _VP]),
+    "dsa_pages_fork_workspace_size": (ctypes.c_size_t, [ctypes.c_int]),
+    "dsa_pages_fork": (ctypes.c_int, [_I32P, _I32P, ctypes.c_int64, _I32P, _I32P, ctypes.c_int, ctypes.c_int, _I32P,
+                                      _I32P, _I32P, ctypes.c_int, _VP, ctypes.c_int, _VP, ctypes.c_size_t, _VP]),
+    "dsa_pages_release": (ctypes.c_int, [_I32P, _I32P, ctypes.c_int64, _I32P, _I32P, ctypes.c_int, ctypes.c_int,
+                                         _I32P, _I32P, ctypes.c_int, _VP]),
+    "dsa_pages_compact_workspace_size": (ctypes.c_size_t, [ctypes.c_int64]),
+    "dsa_pages_compact": (ctypes.c_int, [_I32P, _I32P, ctypes.c_int64, _I32P, _I32P, ctypes.c_int, ctypes.c_int,
+                                         _I32P, _I32P, _VP, ctypes.c_int, _VP, ctypes.c_size_t, _VP]),
     "dsa_window_attn": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int, _I32P,
                                        _I32P, ctypes.c_int, ctypes.c_int, _VP, _F32P, _VP, ctypes.c_size_t, _VP]),
     "dsa_window_decode": (ctypes.c_int, [_VP, _VP, ctypes.c_int64, _I32P, ctypes.c_int, ctypes.c_int, _I32P, _I32P,
@@ -575,6 +583,88 @@ def window_attn_quant(q, kv_cache, kv_scale, block_table, q_pos, window=512, q_r
                                        block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), nq,
                                        int(window), _p(out), _p(lse), _stream()))
     return out
+
+
+MAX_PAGE_POOLS = 8
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+def _page_tables(ref, block_table, ref_out, table_out):
+    _need(ref, torch.int32, name="ref")
+    _need(block_table, torch.int32, name="block_table")
+    if ref.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("ref must be [n_pages], block_table [n_req][max_pages]")
+    ref_out = ref if ref_out is None else ref_out
+    table_out = block_table if table_out is None else table_out
+    _need(ref_out, torch.int32, ref.shape, "ref_out")
+    _need(table_out, torch.int32, block_table.shape, "table_out")
+    return ref_out, table_out
+
+
+def _page_pools(pools, n_pages):
+    if len(pools) > MAX_PAGE_POOLS:
+        raise ValueError(f"at most {MAX_PAGE_POOLS} pools in a call")
+    arr = (_PagePool * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        if not t.is_cuda or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != n_pages:
+            raise ValueError("a pool must be a contiguous CUDA tensor [n_pages][...]")
+        arr[i].data = t.data_ptr()
+        arr[i].page_bytes = t.stride(0) * t.element_size()
+    return arr
+
+
+def pages_fork(ref, block_table, parent, child, length, pools, ref_out=None, table_out=None):
+    """dsa_pages_fork: rows child[i] of block_table [n_req][max_pages] become requests of the first
+    length[i] tokens of rows parent[i]: full pages shared (ref int32 [n_pages] counts holders), a
+    partly filled last one copied to the lowest free page in every pool ([n_pages][...] tensors).
+    In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
+    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
+    n = parent.shape[0]
+    for t, name in ((parent, "parent"), (child, "child"), (length, "length")):
+        _need(t, torch.int32, (n,), name)
+    arr = _page_pools(pools, ref.shape[0])
+    nbytes = lib().dsa_pages_fork_workspace_size(n)
+    ws = _workspace(nbytes, ref.device)
+    _check(lib().dsa_pages_fork(_p(ref), _p(ref_out), ref.shape[0], _p(block_table), _p(table_out),
+                                block_table.shape[1], block_table.shape[0], _p(parent), _p(child), _p(length), n,
+                                ctypes.addressof(arr), len(pools), _p(ws), nbytes, _stream()))
+    return ref_out, table_out
+
+
+def pages_release(ref, block_table, req, keep, ref_out=None, table_out=None):
+    """dsa_pages_release: rows req[i] cut to their first keep[i] tokens, the pages behind given back.
+    In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
+    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
+    n = req.shape[0]
+    _need(req, torch.int32, (n,), "req")
+    _need(keep, torch.int32, (n,), "keep")
+    _check(lib().dsa_pages_release(_p(ref), _p(ref_out), ref.shape[0], _p(block_table), _p(table_out),
+                                   block_table.shape[1], block_table.shape[0], _p(req), _p(keep), n, _stream()))
+    return ref_out, table_out
+
+
+def pages_compact(ref, block_table, pools, ref_out=None, table_out=None, new_index=None, n_live=None):
+    """dsa_pages_compact: the live pages moved to places 0 .. n_live - 1 in every pool, counts and
+    table with them.  In place unless ref_out / table_out are given.  Returns (ref_out, table_out,
+    new_index int32 [n_pages], n_live int32 [1])."""
+    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
+    n_pages = ref.shape[0]
+    if new_index is None:
+        new_index = torch.empty_like(ref)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=ref.device)
+    _need(new_index, torch.int32, (n_pages,), "new_index")
+    _need(n_live, torch.int32, (1,), "n_live")
+    arr = _page_pools(pools, n_pages)
+    nbytes = lib().dsa_pages_compact_workspace_size(n_pages)
+    ws = _workspace(nbytes, ref.device)
+    _check(lib().dsa_pages_compact(_p(ref), _p(ref_out), n_pages, _p(block_table), _p(table_out), block_table.shape[1],
+                                   block_table.shape[0], _p(new_index), _p(n_live), ctypes.addressof(arr), len(pools),
+                                   _p(ws), nbytes, _stream()))
+    return ref_out, table_out, new_index, n_live
 
 
 FRONTEND_ROWS = HI * DI + G * DI + HI      # weight rows: 16 q heads x 256, 4 k groups x 256, 16 gates
