@@ -14,6 +14,7 @@
 #include "attention.cuh"
 #include "attention_cluster.cuh"
 #include "attention_quant.cuh"
+#include "attention_quant_tc.cuh"
 #include "attention_tc.cuh"
 #include "common.cuh"
 #include "compress.cuh"
@@ -1200,8 +1201,8 @@ dsa_status_t attn_quant_attributes()
 {
     static PerDevice attr;
     return attr.once([] {
-        const auto fn = dsa::attnq::sparse_attn_quant_kernel;
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnq::kSmemBytes);
+        const auto fn = dsa::attnqt::sparse_attn_quant_tc_kernel;
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnqt::kSmemBytes);
         return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
 }
@@ -1227,13 +1228,14 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     int sms = 0;
     if ((st = device_info(sms)) != DSA_OK) return st;
     if ((st = attn_quant_attributes()) != DSA_OK) return st;
-    const int resident = dsa::attnq::kCtasPerSm * sms;
+    const int resident = dsa::attnqt::kCtasPerSm * sms;
     CUtensorMap map;
     {
-        // codes as [n_pages * 4 * 8 regions * 16 rows][3][64]: one region (8 K rows, 8 V rows) = box {64, 3, 16}
-        const cuuint64_t dims[3] = {64, 3, (cuuint64_t)n_pages * dsa::kG * (dsa::kPage / dsa::kRegion) * 16};
-        const cuuint64_t strides[2] = {64, (cuuint64_t)dsa::kD};
-        const cuuint32_t box[3] = {64, 3, 16};
+        // codes as [3 blocks][n_pages * 4 * 8 regions * 16 rows][64 dims]: one region (8 K rows, 8 V rows) is
+        // a box {64, 16, 3}, which lands as [block][row][64 B]
+        const cuuint64_t dims[3] = {64, (cuuint64_t)n_pages * dsa::kG * (dsa::kPage / dsa::kRegion) * 16, 3};
+        const cuuint64_t strides[2] = {(cuuint64_t)dsa::kD, 64};
+        const cuuint32_t box[3] = {64, 16, 3};
         if ((st = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv_cache, dims, strides, box,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_64B)) != DSA_OK)
             return st;
@@ -1259,10 +1261,10 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     const int64_t rows = (int64_t)nq * dsa::kG;
     const int most = window > 0 ? window_regions(window) : k;
     p.splits = 1;
-    while (p.splits < 16 && rows * p.splits * 2 <= resident && most >= 2 * p.splits * (dsa::attnq::kTileRegions / 2))
+    while (p.splits < 16 && rows * p.splits * 2 <= resident && most >= 2 * p.splits * (dsa::attnqt::kTileRegions / 2))
         p.splits *= 2;
-    return launch_k("sparse_attn_quant_kernel", dsa::attnq::sparse_attn_quant_kernel,
-                    dim3((unsigned)(rows * p.splits)), dim3(dsa::attnq::kThreads), dsa::attnq::kSmemBytes, stream,
+    return launch_k("sparse_attn_quant_tc_kernel", dsa::attnqt::sparse_attn_quant_tc_kernel,
+                    dim3((unsigned)(rows * p.splits)), dim3(dsa::attnqt::kThreads), dsa::attnqt::kSmemBytes, stream,
                     p.splits > 1 ? (unsigned)p.splits : 0u, map, p);
 }
 }  // namespace

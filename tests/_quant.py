@@ -79,10 +79,12 @@ def attention(q, cache, scale, table, req, pos, tokens):
     """Rows of 64-bit attention and the tolerances of the GPU's.  q float64 [nq][64][192]; tokens(i, g):
     positions attended by row (i, g).  Returns out, lse [nq][64], and out_tol, lse_tol.
 
-    The tolerances count, per head: the score's error d (q as two e4m3 terms, off by at most 2^-18
-    of the head's largest element; 192 fp32 sums; the scaled score and exp2's argument rounded),
-    a weight's relative error 2 d (its own and the sum's), its fp16 rounding (2^-11 relative, or
-    2^-24 of a largest contribution that the reference may trail by 2^8 the other way), and the
+    The tolerances count, per head: the score's error d (q as two e4m3 terms, the second 16 times
+    finer: off by at most 2^-18 of the head's largest element; 192 fp32 sums; the scaled score and exp2's
+    argument rounded), a weight's relative error 2 d (its own and the sum's), its rounding to fp16
+    (2^-11) and from there to three e5m2 terms (of a weight in [1, 2) the first, cut off, leaves less
+    than 2^-2, the second of that less than 2^-5, the third, rounded, at most 2^-9; all three end at the
+    subnormal step 2^-16, half of which is 2^-22 of a largest weight that is at least 2^5), and the
     output's bf16 rounding (2^-8)."""
     nq = q.shape[0]
     out, lse = np.zeros((nq, HQ, D)), np.full((nq, HQ), -np.inf)
@@ -109,10 +111,10 @@ def attention(q, cache, scale, table, req, pos, tokens):
             absqk = np.abs(qq) @ np.abs(k).T / math.sqrt(D)
             d = (2.0 ** -18 * np.abs(qq).max(1)[:, None] * np.abs(k).sum(1)[None] / math.sqrt(D) +
                  192 * 2.0 ** -24 * absqk).max(1) + 2.0 ** -20 * (np.abs(s).max(1) + 1)
-            spread = (w @ np.abs(v))
-            floor = tok.size * 2.0 ** -24 * 448 * (w * sc[:, 1]).max(1)
-            rel = 2.0 ** -11 + np.expm1(2 * d) + 2.0 ** -20
-            out_tol[i, h] = 2.0 ** -8 * np.abs(out[i, h]) + rel[:, None] * spread * (1 + 2.0 ** -8) + floor[:, None]
+            ws = w * sc[:, 1]                                     # weights of the codes
+            rounding = (2.0 ** -9 + 2.0 ** -11) * ws + 2.0 ** -22 * ws.max(1, keepdims=True)
+            spread = np.expm1(2 * d)[:, None] * (w @ np.abs(v)) + rounding @ np.abs(VALUE[cache[page, g, r, 1, row]])
+            out_tol[i, h] = 2.0 ** -8 * np.abs(out[i, h]) + spread * (1 + 2.0 ** -7)
             lse_tol[i, h] = d + 2.0 ** -20 * (1 + np.abs(lse[i, h]))
     return out, lse, out_tol, lse_tol
 
