@@ -79,6 +79,7 @@ struct Params {
     int window;                  // 0: the selection
     float scale_log2;            // log2(e) / sqrt(192)
     int splits;                  // CTAs (the cluster) per row: 1, 2, 4, 8 or 16
+    int per;                     // regions of a row for each of them
 };
 
 // Byte offset of (row, col) in a region's [16 rows: 8 K, 8 V][192 B]: 64-byte lines with the

@@ -34,6 +34,7 @@ struct Smem {
     float red[4][32];
     uint64_t full[kStages], empty[kStages], s_full[2], p_ready, pv_done, q_ready, drain, inbox_bar;
     uint32_t tmem;
+    int state;                                                   // 1: some head has no V yet; 2: O is rescaled
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
 constexpr int kInboxOffset = 16 * 1024;                          // in the ring, behind the staged rows
@@ -111,7 +112,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Lane l of the warp gets f(over the lanes) of v[l] (f: max), 31 shuffles.
+// Lane l of the warp gets the maximum over the lanes of v[l], 31 shuffles.
 __device__ __forceinline__ float reduce_scatter_max32(float (&v)[32])
 {
     const int lane = threadIdx.x & 31;
@@ -143,6 +144,40 @@ __device__ __forceinline__ float reduce_scatter_add16(float (&v)[16])
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
+// A row (query, group) as the CTA `rank` of its cluster sees it.
+struct Row {
+    int g, qi, b, pos, t_lo, row;
+    int j_lo, n_reg, n_tiles;                                    // its regions of the row's, in tiles
+};
+
+// Rows in group-major order: the CTAs at work together gather from one group's share.
+__device__ __forceinline__ Row row_of(const Params &p, unsigned r, int rank, bool report)
+{
+    Row x;
+    x.g = (int)(r / (unsigned)p.nq);
+    x.qi = (int)(r % (unsigned)p.nq);
+    x.row = x.qi * kG + x.g;
+    x.pos = p.q_pos[x.qi];
+    x.b = p.q_req ? p.q_req[x.qi] : x.qi;
+    const int raw = p.window > 0 ? 0 : p.sel_count[x.row];
+    x.t_lo = p.window > 0 ? max(0, x.pos - p.window + 1) : 0;
+    int cnt = 0;                                                 // a query before position 0 attends nothing
+    if (x.pos >= 0) {
+        if (x.b < 0 || x.b >= p.n_req) {
+            if (report) set_error(kErrAttnIndex);
+        } else if (p.window > 0) {
+            cnt = (x.pos >> 3) - (x.t_lo >> 3) + 1;
+        } else {
+            cnt = min(max(raw, 0), p.k);
+            if (report && cnt != raw) set_error(kErrAttnIndex);
+        }
+    }
+    x.j_lo = rank * p.per;
+    x.n_reg = max(0, min(cnt - x.j_lo, p.per));
+    x.n_tiles = (x.n_reg + kTileRegions - 1) / kTileRegions;
+    return x;
+}
+
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     sparse_attn_quant_tc_kernel(const __grid_constant__ CUtensorMap tmap, const Params p)
 {
@@ -169,95 +204,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         fence_mbar_init();
     }
     if (warp == 5) tmem_alloc(&sm.tmem, kTmemCols);
-    pdl_wait();      // the previous kernel's results are visible from here on
-
-    // rows in group-major order: the CTAs resident together gather from one group's share
-    const unsigned rid_row = blockIdx.x / (unsigned)S;
-    const int rank = (int)(blockIdx.x % (unsigned)S);
-    const int g = (int)(rid_row / (unsigned)p.nq), qi = (int)(rid_row % (unsigned)p.nq);
-    const int b = p.q_req ? p.q_req[qi] : qi;
-    const int pos = p.q_pos[qi];
-    const int row = qi * kG + g;
-    const bool bad = pos >= 0 && (b < 0 || b >= p.n_req);
-    const int t_lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    int cnt = 0;                                                 // a query before position 0 attends nothing
-    if (bad) {
-        if (tid == 0) set_error(kErrAttnIndex);
-    } else if (pos >= 0 && p.window > 0) {
-        cnt = (pos >> 3) - (t_lo >> 3) + 1;
-    } else if (pos >= 0) {
-        const int raw = p.sel_count[row];
-        cnt = min(max(raw, 0), p.k);
-        if (tid == 0 && cnt != raw) set_error(kErrAttnIndex);
-    }
-    // this CTA's regions: [j_lo, j_lo + n_reg) of the row's
-    const int per = (cnt + S - 1) / S;
-    const int j_lo = min(cnt, rank * per), n_reg = min(cnt - j_lo, per);
-    const int n_tiles = (n_reg + kTileRegions - 1) / kTileRegions;
     tc_fence_before();
     __syncthreads();                                             // the barriers are set up, TMEM is there
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int64_t head0 = (int64_t)qi * kHQ + g * kHeadsPerGroup;
+    pdl_wait();      // the previous kernel's results are visible from here on
+
+    // This CTA's rows: with S = 1 every gridDim.x-th one (the ring, the barriers' phases and the
+    // tiles' count `base` run through them all), else the cluster's one.
+    const unsigned rows = (unsigned)p.nq * kG;
+    const unsigned first = blockIdx.x / (unsigned)S, step = gridDim.x / (unsigned)S;
+    const int rank = (int)(blockIdx.x % (unsigned)S);
 
     if (warp == 4) {
-        // ---- loads: lane l holds region 32 n + l of the CTA (n: the batch of 2 tiles)
-        auto region_of = [&](int j) -> int {
-            if (j >= n_reg) return -1;
-            return p.window > 0 ? (t_lo >> 3) + j_lo + j : p.sel_idx[(int64_t)row * p.k + j_lo + j];
-        };
-        auto page_of = [&](int j, int r) -> int {
-            if (j >= n_reg) return -1;
-            if (r >= 0 && r / 8 < p.max_pages) {
-                const int page = p.block_table[(int64_t)b * p.max_pages + r / 8];
-                if (page >= 0 && page < p.n_pages) return page;
-            }
-            set_error(kErrAttnIndex);
-            return -1;
-        };
-        auto block_of = [&](int page, int r) { return page < 0 ? -1 : (page * kG + g) * quant::kRegionsPerPage + r % 8; };
-        int r = region_of(lane), block = block_of(page_of(lane, r), r);
-        float2 sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
-        int r_n = region_of(32 + lane), block_n = -1;            // the next batch's
-        float2 sc_n = make_float2(0.0f, 0.0f);
-        int issued = 0;
-        for (int ti = 0; ti < n_tiles; ++ti) {
-            const int st = ti % kStages, sub = ti & 1;
-            if (ti >= kStages &&
-                !__all_sync(0xffffffffu, mbar_wait_sleep(&sm.empty[st], (unsigned)(ti / kStages - 1) & 1u)))
-                break;
-            const bool mine = (lane >> 4) == sub;
-            const unsigned there = __ballot_sync(0xffffffffu, mine && block >= 0);
-            if (lane == 0) {
-                if (there) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(__popc(there) * kRegBytes));
-                else mbar_arrive(&sm.full[st]);
-            }
-            __syncwarp();
-            if (mine) {
-                if (block >= 0)
-                    tma_load_3d(ring + st * kTileBytes + (lane & 15) * kRegBytes, &tmap, 0, block * 16, 0, &sm.full[st]);
-                sm.region[st][lane & 15] = block < 0 ? -1 : r;
-                sm.scale[st][lane & 15] = make_float4(sc.x, sc.y, log2f(sc.y), 0.0f);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[st]);
-            issued = ti + 1;
-            // the next batch's lookups, one dependent load per tile of this batch
-            if (sub == 0) {
-                block_n = block_of(page_of((ti & ~1) * kTileRegions + 32 + lane, r_n), r_n);
-            } else {
-                r = r_n;
-                block = block_n;
-                sc_n = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
-                sc = sc_n;
-                r_n = region_of((ti & ~1) * kTileRegions + 64 + lane);
+        // ---- loads: lane l holds region 32 n + l of the row (n: the batch of 2 tiles)
+        int tg = 0;                                              // tiles before this one, over all rows
+        bool ok = true;
+        for (unsigned rr = first; rr < rows && ok; rr += step) {
+            // (the selection is read beside its count: entries within k lie in the row)
+            auto raw_region = [&](int row, int j_lo, int j) -> int {
+                return p.window > 0 || j_lo + j >= p.k || j >= p.per ? -1 : p.sel_idx[(int64_t)row * p.k + j_lo + j];
+            };
+            const int row = (int)(rr % (unsigned)p.nq) * kG + (int)(rr / (unsigned)p.nq);
+            int r = raw_region(row, rank * p.per, lane), r_n = raw_region(row, rank * p.per, 32 + lane);
+            const Row x = row_of(p, rr, rank, lane == 0 && rank == 0);
+            auto block_of = [&](int j, int &reg) -> int {
+                if (j >= x.n_reg) return -1;
+                if (p.window > 0) reg = (x.t_lo >> 3) + x.j_lo + j;
+                if (reg >= 0 && reg / 8 < p.max_pages) {
+                    const int page = p.block_table[(int64_t)x.b * p.max_pages + reg / 8];
+                    if (page >= 0 && page < p.n_pages) return (page * kG + x.g) * quant::kRegionsPerPage + reg % 8;
+                }
+                set_error(kErrAttnIndex);
+                return -1;
+            };
+            int block = block_of(lane, r), block_n = -1;
+            float2 sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
+            for (int ti = 0; ti < x.n_tiles; ++ti, ++tg) {
+                const int st = tg % kStages, sub = ti & 1;
+                if (tg >= kStages) ok = __all_sync(0xffffffffu, mbar_wait_sleep(&sm.empty[st], (unsigned)(tg / kStages - 1) & 1u));
+                if (!ok) break;
+                const bool mine = (lane >> 4) == sub;
+                const unsigned there = __ballot_sync(0xffffffffu, mine && block >= 0);
+                if (lane == 0) {
+                    if (there) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(__popc(there) * kRegBytes));
+                    else mbar_arrive(&sm.full[st]);
+                }
+                __syncwarp();
+                if (mine) {
+                    if (block >= 0)
+                        tma_load_3d(ring + st * kTileBytes + (lane & 15) * kRegBytes, &tmap, 0, block * 16, 0, &sm.full[st]);
+                    sm.region[st][lane & 15] = block < 0 ? -1 : r;
+                    sm.scale[st][lane & 15] = make_float4(sc.x, sc.y, log2f(sc.y), 0.0f);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[st]);
+                // the next batch's lookups, one dependent load per tile of this batch
+                const int jn = (ti & ~1) * kTileRegions + 32 + lane;
+                if (sub == 0) {
+                    block_n = block_of(jn, r_n);
+                } else {
+                    r = r_n;
+                    block = block_n;
+                    sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
+                    r_n = raw_region(row, x.j_lo, jn + 32);
+                }
             }
         }
         // none of this warp's loads is in flight when the CTA ends, after a wait that gave up as well
         __syncwarp();
         if (lane == 0)
-            for (int s = 0; s < kStages && s < issued; ++s) {
-                const int last = issued - 1 - (issued - 1 - s) % kStages;
+            for (int s = 0; s < kStages && s < tg; ++s) {
+                const int last = tg - 1 - (tg - 1 - s) % kStages;
                 mbar_wait(&sm.full[s], (unsigned)(last / kStages) & 1u);
             }
         __syncwarp();
@@ -265,35 +283,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // ---- MMA issuer (one lane): S(i) as its codes land, O += P'(j) V(j) as the weights are
         // there, whichever is ready; at most two S are ahead of the weights
         if (lane == 0) {
-            bool ok = mbar_wait(&sm.q_ready, 0u);
             // K: rows of 64 bytes, a region's 8 rows 512 bytes, regions 3 KiB apart; V^T: 64-dim blocks
             // 1 KiB apart, 8-token groups 3 KiB apart; P'^T: 8 tokens x 16 heads 128 bytes, terms 2 KiB apart
             const uint32_t k_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring) + 512, 1024);
             const uint32_t q_lo = desc_lo(smem_u32(sm.q), 16), p_lo = desc_lo(smem_u32(sm.p), 128);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kQHi = desc_hi(512, 4), kPHi = desc_hi(2048, 0);
-            int i = 0, j = 0;
+            // the rows of the next S (r_s: i_s of n_s tiles issued) and of the next P' V (r_p)
+            unsigned r_s = first, r_p = first, rows_s = 0;
+            int i_s = 0, i_p = 0, i = 0, j = 0;
+            int n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
+            int reg_p = r_p < rows ? row_of(p, r_p, rank, false).n_reg : 0;
+            bool ok = true;
             long long since = clock64();
-            while (j < n_tiles && ok) {
+            while (ok) {
+                // rows without (further) tiles
+                while (r_s < rows && i_s == n_s) {
+                    r_s += step;
+                    ++rows_s;
+                    i_s = 0;
+                    n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
+                }
+                while (r_p < rows && i_p * kTileRegions >= reg_p) {
+                    r_p += step;
+                    i_p = 0;
+                    reg_p = r_p < rows ? row_of(p, r_p, rank, false).n_reg : 0;
+                }
+                if (r_p >= rows) break;
                 if (j < i && mbar_test(&sm.p_ready, (unsigned)j & 1u)) {
                     tc_fence_after();
                     const uint32_t a = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4);
-                    const int steps = min(4, (n_reg - j * kTileRegions + 3) / 4);          // 32 tokens each
-                    auto step = [&](auto acc, int kk) {
+                    const int steps = min(4, (reg_p - i_p * kTileRegions + 3) / 4);        // 32 tokens each
+                    auto mma = [&](auto acc, int kk) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             mma_f8<decltype(acc)::value>(tmem + kOCol + kNp * h, a + kk * (4 * kRegBytes >> 4) + h * (1024 >> 4),
                                                          kKvHi, p_lo + kk * (512 >> 4), kPHi, kIdescO);
                     };
-                    if (j > 0) step(std::true_type{}, 0);
-                    else step(std::false_type{}, 0);
-                    if (steps > 1) step(std::true_type{}, 1);
-                    if (steps > 2) step(std::true_type{}, 2);
-                    if (steps > 3) step(std::true_type{}, 3);
+                    if (i_p > 0) mma(std::true_type{}, 0);
+                    else mma(std::false_type{}, 0);
+#pragma unroll 1
+                    for (int kk = 1; kk < steps; ++kk) mma(std::true_type{}, kk);
                     umma_commit(&sm.empty[j % kStages]);
                     umma_commit(&sm.pv_done);
                     ++j;
+                    ++i_p;
                     since = clock64();
-                } else if (i < n_tiles && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u)) {
+                } else if (r_s < rows && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u) &&
+                           (i_s > 0 || mbar_test(&sm.q_ready, rows_s & 1u))) {
                     tc_fence_after();
                     const uint32_t a = k_lo + (uint32_t)(i % kStages) * (kTileBytes >> 4), d = tmem + 32 * (i & 1);
                     mma_f8<false>(d, a, kKvHi, q_lo, kQHi, kIdescS);
@@ -303,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                                      q_lo + (((ks >> 1) * (kN * 64) + (ks & 1) * 32) >> 4), kQHi, kIdescS);
                     umma_commit(&sm.s_full[i & 1]);
                     ++i;
+                    ++i_s;
                     since = clock64();
                 } else if (clock64() - since > kWaitLimitCycles) {
                     set_error(kErrWaitTimeout);
@@ -316,236 +353,262 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         __syncwarp();
     } else {
         // ---- softmax: thread = token (TMEM lane) 32 warp + lane of the tile
-        // q of head h: 2^-e q = hi + lo / 16 in e4m3 (warp w: heads 4w .. 4w + 3; lane: 6 elements)
-        {
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (head0 + 4 * warp) * kD) + lane;
-            uint32_t w[4][3];
+        const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
+        bool landed = true;
+        // a wait that gives up leaves the error flag and garbage; the later ones are then short, and
+        // every barrier is still met
+        auto wait = [&](uint64_t *bar, unsigned parity) {
+            if (!mbar_wait(bar, parity, landed ? kWaitLimitCycles : 1ll << 22)) landed = false;
+        };
+        // 2^-e q = hi + lo / 16 in e4m3, for row r: threads 8 h .. 8 h + 7 share head h, thread c
+        // of them holds dims 8 c .. 8 c + 7 of every 64-dim block
+        uint4 qv[3];
+        auto load_q = [&](unsigned r) {
+            const int g = (int)(r / (unsigned)p.nq), qi = (int)(r % (unsigned)p.nq);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((int64_t)qi * kHQ + g * kHeadsPerGroup + (tid >> 3)) * kD + 8 * (tid & 7));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 3; ++j) qv[j] = __ldg(src + 8 * j);
+        };
+        auto put_q = [&]() {
+            const int h = tid >> 3, c = tid & 7;
+            __nv_bfloat162 a2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) w[i][j] = __ldg(src + i * (kD / 2) + 32 * j);
+            for (int j = 0; j < 3; ++j) {
+                const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int h = 4 * warp + i;
-                float a = 0.0f;
+                for (int i = 0; i < 4; ++i) a2 = __hmax2(a2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+            }
+            float a = fmaxf(__low2float(a2), __high2float(a2));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+            const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            if (c == 0) sm.qscale[h] = s * p.scale_log2;
+            uint8_t *dst = sm.q + h * 64 + ((((c >> 1) ^ ((h >> 1) & 3)) << 4) | ((c & 1) << 3));
 #pragma unroll
-                for (int j = 0; j < 3; ++j) a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[i][j])), fabsf(bf16_hi(w[i][j]))));
+            for (int j = 0; j < 3; ++j) {
+                const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-                if (lane == 0) {
-                    sm.qscale[h] = s * p.scale_log2;
-                    sm.m[h] = sm.M[h] = -INFINITY;
-                    sm.mref[h] = sm.c[h] = 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const float x = bf16_lo(w[i]) * inv, y = bf16_hi(w[i]) * inv;
+                    hi[i] = cvt_e4m3x2(x, y);
+                    const uint32_t back = attnq::e4m3x2_to_f16x2((uint16_t)hi[i]);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                    lo[i] = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
                 }
-                // dims 2 lane, 2 lane + 1 of block j
-                const int at = ((((2 * lane) >> 4) ^ ((h >> 1) & 3)) << 4) + ((2 * lane) & 15);
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const float x = bf16_lo(w[i][j]) * inv, y = bf16_hi(w[i][j]) * inv;
-                    const uint32_t hi = cvt_e4m3x2(x, y);
-                    const uint32_t lo = cvt_e4m3x2((x - e4m3_to_f32(hi)) * 16.0f, (y - e4m3_to_f32(hi >> 8)) * 16.0f);
-                    *reinterpret_cast<uint16_t *>(sm.q + j * (kN * 64) + h * 64 + at) = (uint16_t)hi;
-                    *reinterpret_cast<uint16_t *>(sm.q + j * (kN * 64) + (16 + h) * 64 + at) = (uint16_t)lo;
-                }
+                *reinterpret_cast<uint2 *>(dst + j * (kN * 64)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                *reinterpret_cast<uint2 *>(dst + j * (kN * 64) + 16 * 64) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_ready);
+        };
+        int tg = 0;                                              // tiles before this one, over all rows
+        if (first < rows) {
+            load_q(first);
+            put_q();
         }
-        attnq::warps_sync();                                     // qscale and the references
-        const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
-        float2 l[8];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) l[h] = make_float2(0.0f, 0.0f);
-        bool unset = true, landed = true;
-        for (int ti = 0; ti < n_tiles; ++ti) {
-            const int st = ti % kStages;
-            // a wait that gives up leaves the error flag and garbage; the later ones are then short,
-            // and every barrier is still met
-            auto wait = [&](uint64_t *bar, unsigned parity) {
-                if (!mbar_wait(bar, parity, landed ? kWaitLimitCycles : 1ll << 22)) landed = false;
-            };
-            wait(&sm.full[st], (unsigned)(ti / kStages) & 1u);   // (the scales; long there)
-            const int j = 4 * warp + (lane >> 3);
-            const float4 sc = sm.scale[st][j];
-            const int r = sm.region[st][j], tok = 8 * r + (lane & 7);
-            const bool ok = r >= 0 && tok <= pos && tok >= t_lo;
-            const bool all_ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                // a V row that no token attends: zero, whatever it holds
-                uint8_t *v = ring + st * kTileBytes + j * kRegBytes + 512 + (lane & 7) * 64;
-#pragma unroll
-                for (int i = 0; i < 12; ++i) *reinterpret_cast<uint4 *>(v + (i >> 2) * 1024 + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
+        for (unsigned rr = first; rr < rows; rr += step) {
+            const Row x = row_of(p, rr, rank, false);
+            if (tid < 16) {
+                sm.m[tid] = sm.M[tid] = -INFINITY;
+                sm.mref[tid] = sm.c[tid] = 0.0f;
             }
-            wait(&sm.s_full[ti & 1], (unsigned)(ti >> 1) & 1u);
-            __syncwarp();
-            tc_fence_after();
-            float x[32];
-            tmem_ld32(trow + 32 * (ti & 1), x);
-            float2 s[8], pr[8];                                  // scores, weights
-            const float2 ks2 = make_float2(sc.x, sc.x), vs2 = make_float2(sc.y, sc.y);
+            attnq::warps_sync();                                 // the references, qscale
+            float2 l[8];
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const float2 q2 = *reinterpret_cast<const float2 *>(&sm.qscale[2 * h]);
-                const float2 y = ffma2(make_float2(x[16 + 2 * h], x[17 + 2 * h]), make_float2(0.0625f, 0.0625f),
-                                       make_float2(x[2 * h], x[2 * h + 1]));
-                s[h] = fmul2(fmul2(y, ks2), q2);
-            }
-            if (!all_ok) {
-#pragma unroll
-                for (int h = 0; h < 8; ++h)
-                    if (!ok) s[h] = make_float2(-INFINITY, -INFINITY);
-            }
-            bool grow = false;
-            auto weights = [&]() {
-                uint32_t w[8], top = 0u;
-                float2 add = make_float2(0.0f, 0.0f);
-                const float2 one2 = make_float2(1.0f, 1.0f);
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const float2 mr = *reinterpret_cast<const float2 *>(&sm.mref[2 * h]);
-                    const float2 cc = *reinterpret_cast<const float2 *>(&sm.c[2 * h]);
-                    const float2 e = ffma2(s[h], one2, make_float2(-mr.x, -mr.y));
-                    pr[h] = make_float2(ex2(e.x), ex2(e.y));
-                    add = ffma2(pr[h], one2, add);
-                    float2 f = fmul2(vs2, cc);
-                    f = make_float2(fminf(f.x, 8.5070592e37f), fminf(f.y, 8.5070592e37f));     // 2^126
-                    const float2 x2 = fmul2(pr[h], f);
-                    w[h] = attnq::pack_f16x2(x2.x, x2.y);
-                    top = attnq::max_f16x2(top, w[h]);
-                }
-                // three e5m2 terms: the upper bytes of w, of what they leave, and of the rest, rounded
-                uint8_t *dst = sm.p[0] + (32 * warp + lane) * 16;
-#pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    if (term == 2) {
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) w[h] += 0x00800080u;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + term * 2048) =
-                        make_uint4(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531),
-                                   __byte_perm(w[4], w[5], 0x7531), __byte_perm(w[6], w[7], 0x7531));
-                    if (term < 2) {
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) w[h] = hsub2(w[h], w[h] & 0xFF00FF00u);
-                    }
-                }
-                fence_proxy_async();
-                grow = add.x + add.y > kTop || any_above_top(top);
-            };
-            // P' of the tile before has been read
-            if (ti > 0) wait(&sm.pv_done, (unsigned)(ti - 1) & 1u);
-            __syncwarp();
-            if (!unset) weights();
-            tc_fence_before();
-            if (attnq::warps_sync_or(grow || unset)) {
-                // ---- the references move: the tile's maxima of s and s + log2 sV of every head
-                float v[32];
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    v[2 * h] = s[h].x;
-                    v[2 * h + 1] = s[h].y;
-                    v[16 + 2 * h] = s[h].x + sc.z;
-                    v[17 + 2 * h] = s[h].y + sc.z;
-                }
-                sm.red[warp][lane] = reduce_scatter_max32(v);
-                attnq::warps_sync();
-                if (warp == 0) {
-                    float a = lane < 16 ? sm.m[lane] : sm.M[lane - 16];
-                    const float old = a;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) a = fmaxf(a, sm.red[w][lane]);
-                    const float scale = old == a ? 1.0f : exp2f(old - a);
-                    const float d = __shfl_xor_sync(0xffffffffu, a, 16);
-                    if (lane < 16) {
-                        sm.m[lane] = a;
-                        sm.mref[lane] = a == -INFINITY ? 0.0f : a - kBase;
-                        sm.c[lane] = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
-                        sm.al[lane] = scale;
-                    } else {
-                        sm.M[lane - 16] = a;
-                        sm.ao[lane - 16] = scale;
-                    }
-                }
-                attnq::warps_sync();
-                unset = false;
-                bool rescale = false;
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    l[h] = fmul2(l[h], *reinterpret_cast<const float2 *>(&sm.al[2 * h]));
-                    unset |= fminf(sm.M[2 * h], sm.M[2 * h + 1]) == -INFINITY;
-                    rescale |= sm.ao[2 * h] != 1.0f || sm.ao[2 * h + 1] != 1.0f;
-                }
-                if (ti > 0 && rescale) {
-                    // O holds the tiles before this one (their MMAs are done)
-                    tc_fence_after();
+            for (int h = 0; h < 8; ++h) l[h] = make_float2(0.0f, 0.0f);
+            bool unset = true;
+            if (rr + step < rows) load_q(rr + step);             // for the row after this one
+            for (int ti = 0; ti < x.n_tiles; ++ti, ++tg) {
+                const int st = tg % kStages;
+                wait(&sm.full[st], (unsigned)(tg / kStages) & 1u);                         // the scales
+                const int j = 4 * warp + (lane >> 3);
+                const float4 sc = sm.scale[st][j];
+                const int r = sm.region[st][j], tok = 8 * r + (lane & 7);
+                const bool ok = r >= 0 && tok <= x.pos && tok >= x.t_lo;
+                const bool all_ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    // a V row that no token attends: zero, whatever it holds
+                    uint8_t *v = ring + st * kTileBytes + j * kRegBytes + 512 + (lane & 7) * 64;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < 2 * kNp; c0 += 16) {
-                        float o[16];
-                        tmem_ld16(trow + kOCol + c0, o);
-#pragma unroll
-                        for (int h = 0; h < 16; ++h) o[h] *= sm.ao[h];
-                        tmem_st16(trow + kOCol + c0, o);
-                    }
-                    tc_fence_before();
+                    for (int i = 0; i < 12; ++i)
+                        *reinterpret_cast<uint4 *>(v + (i >> 2) * 1024 + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
                 }
-                weights();
-                attnq::warps_sync();
-            }
-#pragma unroll
-            for (int h = 0; h < 8; ++h) l[h] = ffma2(pr[h], make_float2(1.0f, 1.0f), l[h]);
-            if (tid == 0) mbar_arrive(&sm.p_ready);
-        }
-        // ---- the CTA's sums and factors
-        {
-            float v[16];
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                v[2 * h] = l[h].x;
-                v[2 * h + 1] = l[h].y;
-            }
-            const float sum = reduce_scatter_add16(v);
-            if ((lane & 1) == 0) sm.red[warp][lane >> 1] = sum;
-        }
-        attnq::warps_sync();
-        if (warp == 0 && lane < 16) {
-            const float L = (sm.red[0][lane] + sm.red[1][lane]) + (sm.red[2][lane] + sm.red[3][lane]);
-            const float m = sm.m[lane], M = sm.M[lane];
-            // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
-            sm.f[lane] = S > 1 ? L : L > 0.0f ? (M > -INFINITY ? exp2f(M - m) / L : 0.0f) : L;
-            if (S == 1 && p.lse) p.lse[head0 + lane] = L == 0.0f ? -INFINITY : (m - kBase + log2f(L)) * 0.69314718055994531f;
-        }
-        if (n_tiles > 0) {
-            if (!mbar_wait(&sm.pv_done, (unsigned)(n_tiles - 1) & 1u, landed ? kWaitLimitCycles : 1ll << 22)) landed = false;
-        }
-        attnq::warps_sync();                                     // the factors; every warp is past the ring
-        tc_fence_after();
-        float *stage = reinterpret_cast<float *>(ring);
-#pragma unroll 1
-        for (int h2 = 0; h2 < 2; ++h2) {
-            if (h2 == 1 && warp < 2) break;                      // dims 64-127 again
-            float o[16], o1[16], o2[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = o1[i] = o2[i] = 0.0f;
-            if (n_tiles > 0) {
+                wait(&sm.s_full[tg & 1], (unsigned)(tg >> 1) & 1u);
                 __syncwarp();
-                tmem_ld16(trow + kOCol + kNp * h2, o);
-                tmem_ld16(trow + kOCol + kNp * h2 + 16, o1);
-                tmem_ld16(trow + kOCol + kNp * h2 + 32, o2);
-            }
-            const int d = 64 * h2 + 32 * warp + lane;
+                tc_fence_after();
+                float xs[32];
+                tmem_ld32(trow + 32 * (tg & 1), xs);
+                float2 s[8], pr[8];                              // scores, weights
+                const float2 ks2 = make_float2(sc.x, sc.x), vs2 = make_float2(sc.y, sc.y), one2 = make_float2(1.0f, 1.0f);
 #pragma unroll
-            for (int h = 0; h < 16; ++h) {
-                const float y = o[h] + (o1[h] + o2[h]);
-                if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(y * sm.f[h]);
-                else stage[h * kInRow + d] = y;
+                for (int h = 0; h < 8; ++h) {
+                    const float2 q2 = *reinterpret_cast<const float2 *>(&sm.qscale[2 * h]);
+                    const float2 y = ffma2(make_float2(xs[16 + 2 * h], xs[17 + 2 * h]), make_float2(0.0625f, 0.0625f),
+                                           make_float2(xs[2 * h], xs[2 * h + 1]));
+                    s[h] = fmul2(fmul2(y, ks2), q2);
+                }
+                if (!all_ok) {
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        if (!ok) s[h] = make_float2(-INFINITY, -INFINITY);
+                }
+                // P' of the tile before has been read
+                if (tg > 0) wait(&sm.pv_done, (unsigned)(tg - 1) & 1u);
+                __syncwarp();
+#pragma unroll 1
+                for (int pass = unset ? 1 : 0;; pass = 2) {
+                    bool grow = pass == 1;
+                    if (pass != 1) {
+                        // the weights for the references as they are (pass 2: as they have moved)
+                        uint32_t w[8], top = 0u;
+                        float2 add = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            const float2 mr = *reinterpret_cast<const float2 *>(&sm.mref[2 * h]);
+                            const float2 cc = *reinterpret_cast<const float2 *>(&sm.c[2 * h]);
+                            const float2 e = ffma2(s[h], one2, make_float2(-mr.x, -mr.y));
+                            pr[h] = make_float2(ex2(e.x), ex2(e.y));
+                            add = ffma2(pr[h], one2, add);
+                            float2 f = fmul2(vs2, cc);
+                            f = make_float2(fminf(f.x, 8.5070592e37f), fminf(f.y, 8.5070592e37f));         // 2^126
+                            const float2 x2 = fmul2(pr[h], f);
+                            w[h] = attnq::pack_f16x2(x2.x, x2.y);
+                            top = attnq::max_f16x2(top, w[h]);
+                        }
+                        grow = pass == 0 && (add.x + add.y > kTop || any_above_top(top));
+                        // three e5m2 terms: the upper bytes of w, of what they leave, and of the rest, rounded
+                        uint8_t *dst = sm.p[0] + (32 * warp + lane) * 16;
+#pragma unroll
+                        for (int term = 0; term < 3; ++term) {
+                            if (term == 2) {
+#pragma unroll
+                                for (int h = 0; h < 8; ++h) w[h] += 0x00800080u;
+                            }
+                            *reinterpret_cast<uint4 *>(dst + term * 2048) =
+                                make_uint4(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531),
+                                           __byte_perm(w[4], w[5], 0x7531), __byte_perm(w[6], w[7], 0x7531));
+                            if (term < 2) {
+#pragma unroll
+                                for (int h = 0; h < 8; ++h) w[h] = hsub2(w[h], w[h] & 0xFF00FF00u);
+                            }
+                        }
+                        fence_proxy_async();
+                        tc_fence_before();
+                    }
+                    if (!attnq::warps_sync_or(grow)) break;
+                    // ---- the references move: the tile's maxima of s and s + log2 sV of every head
+                    float v[32];
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        v[2 * h] = s[h].x;
+                        v[2 * h + 1] = s[h].y;
+                        v[16 + 2 * h] = s[h].x + sc.z;
+                        v[17 + 2 * h] = s[h].y + sc.z;
+                    }
+                    sm.red[warp][lane] = reduce_scatter_max32(v);
+                    attnq::warps_sync();
+                    if (warp == 0) {
+                        float *ref = lane < 16 ? &sm.m[lane] : &sm.M[lane - 16];
+                        const float old = *ref;
+                        const float a = fmaxf(fmaxf(fmaxf(sm.red[0][lane], sm.red[1][lane]), fmaxf(sm.red[2][lane], sm.red[3][lane])), old);
+                        const float scale = old == a ? 1.0f : exp2f(old - a);
+                        const float d = __shfl_xor_sync(0xffffffffu, a, 16);
+                        *ref = a;
+                        const unsigned none = __ballot_sync(0xffffffffu, lane >= 16 && a == -INFINITY);
+                        const unsigned moved = __ballot_sync(0xffffffffu, lane >= 16 && scale != 1.0f);
+                        if (lane < 16) {
+                            sm.mref[lane] = a == -INFINITY ? 0.0f : a - kBase;
+                            sm.c[lane] = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
+                            sm.al[lane] = scale;
+                        } else {
+                            sm.ao[lane - 16] = scale;
+                        }
+                        if (lane == 0) sm.state = (none ? 1 : 0) | (moved ? 2 : 0);
+                    }
+                    attnq::warps_sync();
+                    unset = (sm.state & 1) != 0;
+                    if (ti > 0) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) l[h] = fmul2(l[h], *reinterpret_cast<const float2 *>(&sm.al[2 * h]));
+                        if (sm.state & 2) {
+                            // O holds the tiles before this one (their MMAs are done)
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < 2 * kNp; c0 += 16) {
+                                float o[16];
+                                tmem_ld16(trow + kOCol + c0, o);
+#pragma unroll
+                                for (int h = 0; h < 16; ++h) o[h] *= sm.ao[h];
+                                tmem_st16(trow + kOCol + c0, o);
+                            }
+                            tc_fence_before();
+                        }
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 8; ++h) l[h] = ffma2(pr[h], one2, l[h]);
+                if (tid == 0) mbar_arrive(&sm.p_ready);
             }
-        }
-        if (S > 1) {
-            if (warp == 0 && lane < 16)
-                *reinterpret_cast<float4 *>(stage + lane * kInRow + kD) = make_float4(sm.m[lane], sm.M[lane], sm.f[lane], 0.0f);
-            fence_proxy_async();                                 // the rows, to the copy engine
+            // every S of this row is done with its q: the next row's
+            if (rr + step < rows) put_q();
+            // ---- the CTA's sums and factors
+            {
+                float v[16];
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    v[2 * h] = l[h].x;
+                    v[2 * h + 1] = l[h].y;
+                }
+                const float sum = reduce_scatter_add16(v);
+                if ((lane & 1) == 0) sm.red[warp][lane >> 1] = sum;
+            }
+            attnq::warps_sync();
+            const int64_t head0 = (int64_t)x.qi * kHQ + x.g * kHeadsPerGroup;
+            if (warp == 0 && lane < 16) {
+                const float L = (sm.red[0][lane] + sm.red[1][lane]) + (sm.red[2][lane] + sm.red[3][lane]);
+                const float m = sm.m[lane], M = sm.M[lane];
+                // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
+                sm.f[lane] = S > 1 ? L : L > 0.0f ? (M > -INFINITY ? exp2f(M - m) / L : 0.0f) : L;
+                if (S == 1 && p.lse) p.lse[head0 + lane] = L == 0.0f ? -INFINITY : (m - kBase + log2f(L)) * 0.69314718055994531f;
+            }
+            if (x.n_tiles > 0) wait(&sm.pv_done, (unsigned)(tg - 1) & 1u);
+            attnq::warps_sync();                                 // the factors; every warp is past the ring (S > 1)
+            tc_fence_after();
+            float *stage = reinterpret_cast<float *>(ring);
+#pragma unroll 1
+            for (int h2 = 0; h2 < 2; ++h2) {
+                if (h2 == 1 && warp < 2) break;                  // dims 64-127 again
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+                __syncwarp();
+                if (x.n_tiles > 0) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kNp; c0 += 16) {
+                        float o1[16];
+                        tmem_ld16(trow + kOCol + kNp * h2 + c0, o1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] += o1[i];
+                    }
+                }
+                const int d = 64 * h2 + 32 * warp + lane;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) {
+                    if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h]);
+                    else stage[h * kInRow + d] = o[h];
+                }
+            }
+            if (S > 1) {
+                if (warp == 0 && lane < 16)
+                    *reinterpret_cast<float4 *>(stage + lane * kInRow + kD) = make_float4(sm.m[lane], sm.M[lane], sm.f[lane], 0.0f);
+                fence_proxy_async();                             // the rows, to the copy engine
+            }
+            tc_fence_before();
+            attnq::warps_sync();                                 // before the references are set again
         }
     }
     tc_fence_before();
@@ -567,9 +630,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         bulk_commit();
     }
     const bool inbox_ok = mbar_wait(&sm.inbox_bar, 0u);          // false: error set
+    const int64_t head0 = (int64_t)(first % (unsigned)p.nq) * kHQ + (int)(first / (unsigned)p.nq) * kHeadsPerGroup;
     for (int e = tid; inbox_ok && e < per_cta * (kD / 2); e += kThreads) {
         const int j = e / (kD / 2), d = 2 * (e % (kD / 2));
         float mm = -INFINITY, MM = -INFINITY;
+#pragma unroll 4
         for (int cc = 0; cc < S; ++cc) {
             const float *in = inbox + (cc * per_cta + j) * kInRow;
             mm = fmaxf(mm, in[kD]);
@@ -577,11 +642,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         const float mref = mm == -INFINITY ? 0.0f : mm, Mref = MM == -INFINITY ? 0.0f : MM;
         float Ls = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll 4
         for (int cc = 0; cc < S; ++cc) {
             const float *in = inbox + (cc * per_cta + j) * kInRow;
             const float2 v = *reinterpret_cast<const float2 *>(in + d);
-            const float wt = exp2f(in[kD + 1] - Mref);
-            Ls += exp2f(in[kD] - mref) * in[kD + 2];
+            const float wt = ex2(in[kD + 1] - Mref);
+            Ls += ex2(in[kD] - mref) * in[kD + 2];
             x += wt * v.x;
             y += wt * v.y;
         }

@@ -1263,8 +1263,10 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     p.splits = 1;
     while (p.splits < 16 && rows * p.splits * 2 <= resident && most >= 2 * p.splits * (dsa::attnqt::kTileRegions / 2))
         p.splits *= 2;
-    return launch_k("sparse_attn_quant_tc_kernel", dsa::attnqt::sparse_attn_quant_tc_kernel,
-                    dim3((unsigned)(rows * p.splits)), dim3(dsa::attnqt::kThreads), dsa::attnqt::kSmemBytes, stream,
+    p.per = (most + p.splits - 1) / p.splits;
+    // one CTA after another takes the rows where there are more than CTAs at once
+    const int64_t ctas = p.splits > 1 ? rows * p.splits : std::min<int64_t>(rows, resident);
+    return launch_k("sparse_attn_quant_tc_kernel", dsa::attnqt::sparse_attn_quant_tc_kernel, dim3((unsigned)ctas), dim3(dsa::attnqt::kThreads), dsa::attnqt::kSmemBytes, stream,
                     p.splits > 1 ? (unsigned)p.splits : 0u, map, p);
 }
 }  // namespace
