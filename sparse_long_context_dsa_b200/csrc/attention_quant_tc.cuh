@@ -1,6 +1,8 @@
 // (header comment written once the kernel is settled)
 #pragma once
 
+#include <type_traits>
+
 #include "attention_quant.cuh"
 
 namespace dsa {
@@ -17,7 +19,8 @@ constexpr int kStages = 2;
 constexpr int kThreads = 192;                                    // warps 0-3 softmax, 4 loads, 5 MMA
 constexpr int kCtasPerSm = 2;
 constexpr int kN = 32;                                           // S: 16 heads x (hi, lo) of q
-constexpr int kOCol = 64;                                        // TMEM: S 0, 32 (two buffers); O 64 .. 255 (192 dims)
+constexpr int kNp = 48;                                          // O: 16 heads x three terms of P'
+constexpr int kOCol = 64;                                        // TMEM: S 0, 32 (two buffers); O 64 (dims 0-127), 112 (64-191)
 constexpr int kTmemCols = 256;
 constexpr float kBase = 5.0f;                                    // log2 of a weight at its reference
 constexpr float kTop = 32768.0f;                                 // 2^15: the largest P' before the references move
@@ -56,9 +59,8 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi,
         : "memory");
 }
 constexpr uint32_t kIdescS = umma_idesc_e4m3(128, kN);
-// P' (A: 16 heads x three terms, e5m2; M = 64, its last 16 rows meet what lies behind the terms and
-// are never read) and V^T (B, e4m3), both MN-major
-constexpr uint32_t kIdescO = umma_idesc_e4m3(64, kD) | (1u << 7) | (1u << 15) | (1u << 16);
+// V^T (A, e4m3) and P'^T (B, e5m2) MN-major
+constexpr uint32_t kIdescO = umma_idesc_e4m3(128, kNp) | (1u << 10) | (1u << 15) | (1u << 16);
 
 // Whether the phase of `bar` with the given parity is complete; never suspends.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned parity)
@@ -86,16 +88,26 @@ __device__ __forceinline__ bool any_above_top(uint32_t v)
     return __hgt2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0x7800))) != 0u;
 }
 
-// 32 consecutive fp32 columns of this warp's 32 TMEM lanes written from registers.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per lane).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
         ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-          "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-          "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-          "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+          "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -216,17 +228,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int row = (int)(rr % (unsigned)p.nq) * kG + (int)(rr / (unsigned)p.nq);
             int r = raw_region(row, rank * p.per, lane), r_n = raw_region(row, rank * p.per, 32 + lane);
             const Row x = row_of(p, rr, rank, lane == 0 && rank == 0);
-            auto block_of = [&](int j, int &reg) -> int {
+            // the page of region j, and (once it is there) its block
+            auto page_of = [&](int j, int &reg) -> int {
                 if (j >= x.n_reg) return -1;
                 if (p.window > 0) reg = (x.t_lo >> 3) + x.j_lo + j;
-                if (reg >= 0 && reg / 8 < p.max_pages) {
-                    const int page = p.block_table[(int64_t)x.b * p.max_pages + reg / 8];
-                    if (page >= 0 && page < p.n_pages) return (page * kG + x.g) * quant::kRegionsPerPage + reg % 8;
-                }
+                return reg >= 0 && reg / 8 < p.max_pages ? p.block_table[(int64_t)x.b * p.max_pages + reg / 8] : -1;
+            };
+            auto block_of = [&](int j, int reg, int page) -> int {
+                if (j >= x.n_reg) return -1;
+                if (page >= 0 && page < p.n_pages) return (page * kG + x.g) * quant::kRegionsPerPage + reg % 8;
                 set_error(kErrAttnIndex);
                 return -1;
             };
-            int block = block_of(lane, r), block_n = -1;
+            int page_n = page_of(lane, r);
+            int block = block_of(lane, r, page_n);
             float2 sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
             for (int ti = 0; ti < x.n_tiles; ++ti, ++tg) {
                 const int st = tg % kStages, sub = ti & 1;
@@ -247,13 +262,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[st]);
-                // the next batch's lookups, one dependent load per tile of this batch
+                // the next batch's lookups: no load is waited for in the tile that issues it
                 const int jn = (ti & ~1) * kTileRegions + 32 + lane;
                 if (sub == 0) {
-                    block_n = block_of(jn, r_n);
+                    page_n = page_of(jn, r_n);
                 } else {
                     r = r_n;
-                    block = block_n;
+                    block = block_of(jn, r, page_n);
                     sc = block < 0 ? make_float2(0.0f, 0.0f) : __ldg(p.scale + block);
                     r_n = raw_region(row, x.j_lo, jn + 32);
                 }
@@ -301,12 +316,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     tc_fence_after();
                     const uint32_t a = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4);
                     const int steps = min(4, (reg_p - i_p * kTileRegions + 3) / 4);        // 32 tokens each
-                    if (i_p > 0) mma_f8<true>(tmem + kOCol, p_lo, kPHi, a, kKvHi, kIdescO);
-                    else mma_f8<false>(tmem + kOCol, p_lo, kPHi, a, kKvHi, kIdescO);
+                    auto mma = [&](auto acc, int kk) {
 #pragma unroll
-                    for (int kk = 1; kk < 4; ++kk)
-                        if (kk < steps)
-                            mma_f8<true>(tmem + kOCol, p_lo + kk * (512 >> 4), kPHi, a + kk * (4 * kRegBytes >> 4), kKvHi, kIdescO);
+                        for (int h = 0; h < 2; ++h)
+                            mma_f8<decltype(acc)::value>(tmem + kOCol + kNp * h, a + kk * (4 * kRegBytes >> 4) + h * (1024 >> 4),
+                                                         kKvHi, p_lo + kk * (512 >> 4), kPHi, kIdescO);
+                    };
+                    if (i_p > 0) mma(std::true_type{}, 0);
+                    else mma(std::false_type{}, 0);
+#pragma unroll 1
+                    for (int kk = 1; kk < steps; ++kk) mma(std::true_type{}, kk);
                     umma_commit(&sm.empty[j % kStages]);
                     umma_commit(&sm.pv_done);
                     ++j;
@@ -526,14 +545,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         if (sm.state & 2) {
                             // O holds the tiles before this one (their MMAs are done)
                             tc_fence_after();
-                            const float f = sm.ao[lane & 15];
 #pragma unroll 1
-                            for (int c0 = 0; warp < 3 && c0 < kD; c0 += 32) {
-                                float o[32];
-                                tmem_ld32(trow + kOCol + c0, o);
+                            for (int c0 = 0; c0 < 2 * kNp; c0 += 16) {
+                                float o[16];
+                                tmem_ld16(trow + kOCol + c0, o);
 #pragma unroll
-                                for (int h = 0; h < 32; ++h) o[h] *= f;
-                                tmem_st32(trow + kOCol + c0, o);
+                                for (int h = 0; h < 16; ++h) o[h] *= sm.ao[h];
+                                tmem_st16(trow + kOCol + c0, o);
                             }
                             tc_fence_before();
                         }
@@ -569,36 +587,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             attnq::warps_sync();                                 // the factors; every warp is past the ring (S > 1)
             tc_fence_after();
             float *stage = reinterpret_cast<float *>(ring);
-            // O: term w of head lane in lanes 0-15 of warp w < 3; 32 dims at a time through the P' tile
-            float4 *buf = reinterpret_cast<float4 *>(sm.p);      // [term][head][8 chunks, XORed by the head]
 #pragma unroll 1
-            for (int c0 = 0; c0 < kD; c0 += 32) {
-                if (warp < 3) {
-                    float o[32];
-                    if (x.n_tiles > 0) {
-                        tmem_ld32(trow + kOCol + c0, o);
-                    } else {
+            for (int h2 = 0; h2 < 2; ++h2) {
+                if (h2 == 1 && warp < 2) break;                  // dims 64-127 again
+                float o[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-                    }
-                    if (lane < 16) {
+                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+                __syncwarp();
+                if (x.n_tiles > 0) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kNp; c0 += 16) {
+                        float o1[16];
+                        tmem_ld16(trow + kOCol + kNp * h2 + c0, o1);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            buf[(warp * 16 + lane) * 8 + (i ^ (lane & 7))] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 16; ++i) o[i] += o1[i];
                     }
                 }
-                attnq::warps_sync();
-                const int h = tid >> 3, c = (tid & 7) ^ (h & 7);
-                const float4 u = buf[h * 8 + c], v = buf[(16 + h) * 8 + c], w = buf[(32 + h) * 8 + c];
-                const float4 y = make_float4(u.x + (v.x + w.x), u.y + (v.y + w.y), u.z + (v.z + w.z), u.w + (v.w + w.w));
-                if (S == 1) {
-                    const float f = sm.f[h];
-                    *reinterpret_cast<uint2 *>(p.out + (head0 + h) * kD + c0 + 4 * (tid & 7)) =
-                        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-                } else {
-                    *reinterpret_cast<float4 *>(stage + h * kInRow + c0 + 4 * (tid & 7)) = y;
+                const int d = 64 * h2 + 32 * warp + lane;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) {
+                    if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h]);
+                    else stage[h * kInRow + d] = o[h];
                 }
-                attnq::warps_sync();
             }
             if (S > 1) {
                 if (warp == 0 && lane < 16)
@@ -606,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 fence_proxy_async();                             // the rows, to the copy engine
             }
             tc_fence_before();
+            attnq::warps_sync();                                 // before the references are set again
         }
     }
     tc_fence_before();
@@ -628,36 +639,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     const bool inbox_ok = mbar_wait(&sm.inbox_bar, 0u);          // false: error set
     const int64_t head0 = (int64_t)(first % (unsigned)p.nq) * kHQ + (int)(first / (unsigned)p.nq) * kHeadsPerGroup;
-    // factors of the 16 rows (source cc, head slot j): 2^(M_cc - M), and the sums
-    if (inbox_ok && tid < kHeadsPerGroup) {
-        const int j = tid % per_cta;
+    for (int e = tid; inbox_ok && e < per_cta * (kD / 2); e += kThreads) {
+        const int j = e / (kD / 2), d = 2 * (e % (kD / 2));
         float mm = -INFINITY, MM = -INFINITY;
 #pragma unroll 4
         for (int cc = 0; cc < S; ++cc) {
-            const float2 v = *reinterpret_cast<const float2 *>(inbox + (cc * per_cta + j) * kInRow + kD);
-            mm = fmaxf(mm, v.x);
-            MM = fmaxf(MM, v.y);
+            const float *in = inbox + (cc * per_cta + j) * kInRow;
+            mm = fmaxf(mm, in[kD]);
+            MM = fmaxf(MM, in[kD + 1]);
         }
         const float mref = mm == -INFINITY ? 0.0f : mm, Mref = MM == -INFINITY ? 0.0f : MM;
-        const float *in = inbox + tid * kInRow + kD;
-        float Ls = ex2(in[0] - mref) * in[2];
-        for (int o = kHeadsPerGroup / 2; o >= per_cta; o >>= 1) Ls += __shfl_xor_sync(0xffffu, Ls, o);
-        const float f = Ls > 0.0f ? (MM > -INFINITY ? exp2f(MM - mm) / Ls : 0.0f) : Ls;
-        sm.f[tid] = ex2(in[1] - Mref) * f;
-        if (p.lse && tid < per_cta)
-            p.lse[head0 + rank + S * j] = Ls == 0.0f ? -INFINITY : (mm - kBase + log2f(Ls)) * 0.69314718055994531f;
-    }
-    __syncthreads();
-    for (int e = tid; inbox_ok && e < per_cta * (kD / 2); e += kThreads) {
-        const int j = e / (kD / 2), d = 2 * (e % (kD / 2));
-        float x = 0.0f, y = 0.0f;
-#pragma unroll 8
+        float Ls = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll 4
         for (int cc = 0; cc < S; ++cc) {
-            const float2 v = *reinterpret_cast<const float2 *>(inbox + (cc * per_cta + j) * kInRow + d);
-            x += sm.f[cc * per_cta + j] * v.x;
-            y += sm.f[cc * per_cta + j] * v.y;
+            const float *in = inbox + (cc * per_cta + j) * kInRow;
+            const float2 v = *reinterpret_cast<const float2 *>(in + d);
+            const float wt = ex2(in[kD + 1] - Mref);
+            Ls += ex2(in[kD] - mref) * in[kD + 2];
+            x += wt * v.x;
+            y += wt * v.y;
         }
-        *reinterpret_cast<uint32_t *>(p.out + (head0 + rank + S * j) * kD + d) = pack_bf16x2(x, y);
+        const float f = Ls > 0.0f ? (MM > -INFINITY ? exp2f(MM - mm) / Ls : 0.0f) : Ls;
+        const int64_t head = head0 + rank + S * j;
+        *reinterpret_cast<uint32_t *>(p.out + head * kD + d) = pack_bf16x2(x * f, y * f);
+        if (p.lse && d == 0) p.lse[head] = Ls == 0.0f ? -INFINITY : (mm - kBase + log2f(Ls)) * 0.69314718055994531f;
     }
     // this CTA's copies have read their rows before its shared memory goes away
     if (warp == 0 && lane < kHeadsPerGroup) bulk_wait_read_all();
