@@ -1,4 +1,5 @@
-"""Builds libdsa.so (the CUDA kernels and their C-ABI) in-tree for sm_100a with nvcc.
+"""Builds libdsa.so (the CUDA kernels and their C-ABI) in-tree for sm_100a with nvcc, and _calls.so
+(native argument marshalling for the Python binding) beside it with g++.
 
     python -m sparse_long_context_dsa_b200.build [--force]
 """
@@ -12,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdsa.so")
+CALLS = os.path.join(HERE, "_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-warn-spills"]
@@ -25,7 +27,28 @@ def sources():
     return out
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    src = [os.path.join(CSRC, "calls.cpp"), os.path.join(ROOT, "include", "dsa.h")]
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(s) for s in src):
+        return CALLS
+    import sysconfig
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *["-I" + i for i in inc], src[0], "-o", tmp,
+           "-L" + os.path.join(t, "lib"), "-Wl,-rpath," + os.path.join(t, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force, verbose)
     newest = max(os.path.getmtime(s) for s in sources())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB

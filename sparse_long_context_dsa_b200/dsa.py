@@ -22,6 +22,7 @@ Q_FP8 = 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
 _lib = None
+_calls = None                      # native marshalling of the quantised-cache and page calls (csrc/calls.cpp)
 _lock = threading.Lock()
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = range(6)
@@ -121,6 +122,26 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = L
     return _lib
+
+
+def _native():
+    """The _calls extension, bound to libdsa.  Its functions return the call's status, or -1 (nothing
+    called) for arguments that the checks here then name."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _calls as ext
+        except ImportError as e:
+            raise ImportError("the _calls extension is missing or does not load: build it with "
+                              "`python -m sparse_long_context_dsa_b200.build`") from e
+        ext.bind(LIB_PATH)
+        _calls = ext
+    return _calls
+
+
+def _refused(name):
+    raise ValueError(f"{name}: an argument is not what the call takes")
 
 
 def exported_symbols():
@@ -516,133 +537,112 @@ def kv_append_quant(kv_cache, kv_scale, block_table, q_pos, new_k, new_v, q_req=
     """dsa_kv_append_quant: token i's K and V rows (new_k, new_v bf16 [n][4][192]) quantised into the
     8-bit cache at position q_pos[i] of request q_req[i] (or i).  Tokens of one region are
     neighbours in the list, in ascending order."""
-    _quant_cache_args(kv_cache, kv_scale, block_table)
-    n = q_pos.shape[0]
-    _need(q_pos, torch.int32, (n,), "q_pos")
-    _need(new_k, torch.bfloat16, (n, G, D), "new_k")
-    _need(new_v, torch.bfloat16, (n, G, D), "new_v")
-    if q_req is not None:
-        _need(q_req, torch.int32, (n,), "q_req")
-    elif n > block_table.shape[0]:
-        raise ValueError("without q_req token i is request i's: block_table needs a row for each")
-    _check(lib().dsa_kv_append_quant(_p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
-                                     block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), n, _p(new_k),
-                                     _p(new_v), _stream()))
+    st = _native().kv_append_quant(kv_cache, kv_scale, block_table, q_pos, new_k, new_v, q_req)
+    if st < 0:
+        _quant_cache_args(kv_cache, kv_scale, block_table)
+        n = q_pos.shape[0]
+        _need(q_pos, torch.int32, (n,), "q_pos")
+        _need(new_k, torch.bfloat16, (n, G, D), "new_k")
+        _need(new_v, torch.bfloat16, (n, G, D), "new_v")
+        if q_req is not None:
+            _need(q_req, torch.int32, (n,), "q_req")
+        elif n > block_table.shape[0]:
+            raise ValueError("without q_req token i is request i's: block_table needs a row for each")
+        _refused("kv_append_quant")
+    _check(st)
 
 
-def _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse):
-    nq = q.shape[0]
-    _need(q, torch.bfloat16, (nq, HQ, D), "q")
-    _quant_cache_args(kv_cache, kv_scale, block_table)
-    _need(q_pos, torch.int32, (nq,), "q_pos")
-    if q_req is not None:
-        _need(q_req, torch.int32, (nq,), "q_req")
-    elif nq > block_table.shape[0]:
-        raise ValueError("without q_req query i is request i's: block_table needs a row for each")
+def _attn_quant(name, q, kv_cache, kv_scale, block_table, q_req, q_pos, sel_idx, sel_count, window, out, lse):
     if out is None:
-        out = torch.empty((nq, HQ, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, (nq, HQ, D), "out")
-    if lse is not None:
-        _need(lse, torch.float32, (nq, HQ), "lse")
-    return nq, out
-
-
-def _selection_args(nq, sel_idx, sel_count):
-    _need(sel_idx, torch.int32, name="sel_idx")
-    k = sel_idx.shape[-1]
-    _need(sel_idx, torch.int32, (nq, G, k), "sel_idx")
-    _need(sel_count, torch.int32, (nq, G), "sel_count")
-    return k
+        out = torch.empty((q.shape[0], HQ, D), dtype=torch.bfloat16, device=q.device)
+    st = _native().attn_quant(q, kv_cache, kv_scale, block_table, q_req, q_pos, sel_idx, sel_count, window, out, lse)
+    if st < 0:
+        nq = q.shape[0]
+        _need(q, torch.bfloat16, (nq, HQ, D), "q")
+        _quant_cache_args(kv_cache, kv_scale, block_table)
+        _need(q_pos, torch.int32, (nq,), "q_pos")
+        if q_req is not None:
+            _need(q_req, torch.int32, (nq,), "q_req")
+        elif nq > block_table.shape[0]:
+            raise ValueError("without q_req query i is request i's: block_table needs a row for each")
+        if sel_idx is not None:
+            _need(sel_idx, torch.int32, (nq, G, sel_idx.shape[-1]), "sel_idx")
+            _need(sel_count, torch.int32, (nq, G), "sel_count")
+        _need(out, torch.bfloat16, (nq, HQ, D), "out")
+        if lse is not None:
+            _need(lse, torch.float32, (nq, HQ), "lse")
+        _refused(name)
+    _check(st)
+    return out
 
 
 def sparse_attn_decode_quant(q, kv_cache, kv_scale, block_table, q_pos, sel_idx, sel_count, out=None, lse=None):
     """sparse_attn_decode over the 8-bit cache: one query per request.  Returns out bf16 [B][64][192]."""
-    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, None, out, lse)
-    k = _selection_args(nq, sel_idx, sel_count)
-    _check(lib().dsa_sparse_attn_decode_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
-                                              block_table.shape[1], _p(q_pos), nq, _p(sel_idx), _p(sel_count), k,
-                                              _p(out), _p(lse), _stream()))
-    return out
+    return _attn_quant("sparse_attn_decode_quant", q, kv_cache, kv_scale, block_table, None, q_pos, sel_idx, sel_count,
+                       0, out, lse)
 
 
 def sparse_attn_prefill_quant(q, kv_cache, kv_scale, block_table, q_req, q_pos, sel_idx, sel_count, out=None,
                               lse=None):
     """sparse_attn_prefill over the 8-bit cache: queries of several requests.  Returns out."""
-    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse)
-    k = _selection_args(nq, sel_idx, sel_count)
-    _check(lib().dsa_sparse_attn_prefill_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
-                                               block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), nq,
-                                               _p(sel_idx), _p(sel_count), k, _p(out), _p(lse), _stream()))
-    return out
+    if q_req is None:
+        raise ValueError("q_req must not be None")
+    return _attn_quant("sparse_attn_prefill_quant", q, kv_cache, kv_scale, block_table, q_req, q_pos, sel_idx,
+                       sel_count, 0, out, lse)
 
 
 def window_attn_quant(q, kv_cache, kv_scale, block_table, q_pos, window=512, q_req=None, out=None, lse=None):
     """window_attn over the 8-bit cache.  Returns out bf16 [nq][64][192]."""
-    nq, out = _attn_quant_args(q, kv_cache, kv_scale, block_table, q_pos, q_req, out, lse)
-    _check(lib().dsa_window_attn_quant(_p(q), _p(kv_cache), _p(kv_scale), kv_cache.shape[0], _p(block_table),
-                                       block_table.shape[1], block_table.shape[0], _p(q_req), _p(q_pos), nq,
-                                       int(window), _p(out), _p(lse), _stream()))
-    return out
+    return _attn_quant("window_attn_quant", q, kv_cache, kv_scale, block_table, q_req, q_pos, None, None, int(window),
+                       out, lse)
 
 
 MAX_PAGE_POOLS = 8
 
 
-class _PagePool(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
-
-
-def _page_tables(ref, block_table, ref_out, table_out):
+def _page_args(ref, block_table, ref_out, table_out, lists=(), pools=()):
+    """Names the argument that the page calls do not take."""
     _need(ref, torch.int32, name="ref")
     _need(block_table, torch.int32, name="block_table")
     if ref.dim() != 1 or block_table.dim() != 2:
         raise ValueError("ref must be [n_pages], block_table [n_req][max_pages]")
-    ref_out = ref if ref_out is None else ref_out
-    table_out = block_table if table_out is None else table_out
-    _need(ref_out, torch.int32, ref.shape, "ref_out")
-    _need(table_out, torch.int32, block_table.shape, "table_out")
-    return ref_out, table_out
-
-
-def _page_pools(pools, n_pages):
+    _need(ref_out, torch.int32, tuple(ref.shape), "ref_out")
+    _need(table_out, torch.int32, tuple(block_table.shape), "table_out")
+    for t, name in lists:
+        _need(t, torch.int32, tuple(lists[0][0].shape[:1]), name)
     if len(pools) > MAX_PAGE_POOLS:
         raise ValueError(f"at most {MAX_PAGE_POOLS} pools in a call")
-    arr = (_PagePool * max(1, len(pools)))()
-    for i, t in enumerate(pools):
-        if not t.is_cuda or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != n_pages:
+    for t in pools:
+        if not t.is_cuda or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != ref.shape[0]:
             raise ValueError("a pool must be a contiguous CUDA tensor [n_pages][...]")
-        arr[i].data = t.data_ptr()
-        arr[i].page_bytes = t.stride(0) * t.element_size()
-    return arr
 
 
 def pages_fork(ref, block_table, parent, child, length, pools, ref_out=None, table_out=None):
     """dsa_pages_fork: rows child[i] of block_table [n_req][max_pages] become requests of the first
     length[i] tokens of rows parent[i]: full pages shared (ref int32 [n_pages] counts holders), a
-    partly filled last one copied to the lowest free page in every pool ([n_pages][...] tensors).
-    In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
-    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
-    n = parent.shape[0]
-    for t, name in ((parent, "parent"), (child, "child"), (length, "length")):
-        _need(t, torch.int32, (n,), name)
-    arr = _page_pools(pools, ref.shape[0])
-    nbytes = lib().dsa_pages_fork_workspace_size(n)
-    ws = _workspace(nbytes, ref.device)
-    _check(lib().dsa_pages_fork(_p(ref), _p(ref_out), ref.shape[0], _p(block_table), _p(table_out),
-                                block_table.shape[1], block_table.shape[0], _p(parent), _p(child), _p(length), n,
-                                ctypes.addressof(arr), len(pools), _p(ws), nbytes, _stream()))
+    partly filled last one copied to the lowest free page in every pool (a list of [n_pages][...]
+    tensors).  In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
+    ref_out = ref if ref_out is None else ref_out
+    table_out = block_table if table_out is None else table_out
+    st = _native().pages_fork(ref, block_table, parent, child, length, pools, ref_out, table_out)
+    if st < 0:
+        _page_args(ref, block_table, ref_out, table_out, ((parent, "parent"), (child, "child"), (length, "length")),
+                   pools)
+        _refused("pages_fork")
+    _check(st)
     return ref_out, table_out
 
 
 def pages_release(ref, block_table, req, keep, ref_out=None, table_out=None):
     """dsa_pages_release: rows req[i] cut to their first keep[i] tokens, the pages behind given back.
     In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
-    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
-    n = req.shape[0]
-    _need(req, torch.int32, (n,), "req")
-    _need(keep, torch.int32, (n,), "keep")
-    _check(lib().dsa_pages_release(_p(ref), _p(ref_out), ref.shape[0], _p(block_table), _p(table_out),
-                                   block_table.shape[1], block_table.shape[0], _p(req), _p(keep), n, _stream()))
+    ref_out = ref if ref_out is None else ref_out
+    table_out = block_table if table_out is None else table_out
+    st = _native().pages_release(ref, block_table, req, keep, ref_out, table_out)
+    if st < 0:
+        _page_args(ref, block_table, ref_out, table_out, ((req, "req"), (keep, "keep")))
+        _refused("pages_release")
+    _check(st)
     return ref_out, table_out
 
 
@@ -650,20 +650,19 @@ def pages_compact(ref, block_table, pools, ref_out=None, table_out=None, new_ind
     """dsa_pages_compact: the live pages moved to places 0 .. n_live - 1 in every pool, counts and
     table with them.  In place unless ref_out / table_out are given.  Returns (ref_out, table_out,
     new_index int32 [n_pages], n_live int32 [1])."""
-    ref_out, table_out = _page_tables(ref, block_table, ref_out, table_out)
-    n_pages = ref.shape[0]
+    ref_out = ref if ref_out is None else ref_out
+    table_out = block_table if table_out is None else table_out
     if new_index is None:
         new_index = torch.empty_like(ref)
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=ref.device)
-    _need(new_index, torch.int32, (n_pages,), "new_index")
-    _need(n_live, torch.int32, (1,), "n_live")
-    arr = _page_pools(pools, n_pages)
-    nbytes = lib().dsa_pages_compact_workspace_size(n_pages)
-    ws = _workspace(nbytes, ref.device)
-    _check(lib().dsa_pages_compact(_p(ref), _p(ref_out), n_pages, _p(block_table), _p(table_out), block_table.shape[1],
-                                   block_table.shape[0], _p(new_index), _p(n_live), ctypes.addressof(arr), len(pools),
-                                   _p(ws), nbytes, _stream()))
+    st = _native().pages_compact(ref, block_table, pools, ref_out, table_out, new_index, n_live)
+    if st < 0:
+        _page_args(ref, block_table, ref_out, table_out, (), pools)
+        _need(new_index, torch.int32, tuple(ref.shape), "new_index")
+        _need(n_live, torch.int32, (1,), "n_live")
+        _refused("pages_compact")
+    _check(st)
     return ref_out, table_out, new_index, n_live
 
 

@@ -1,6 +1,4 @@
 """The page calls' refusals, without a GPU."""
-import ctypes
-
 import pytest
 import torch
 
@@ -14,13 +12,6 @@ P = 1 << 20                        # an address that is never read: these calls 
 def lib():
     B.build()
     return dsa.lib()
-
-
-def pool(data, page_bytes, n=1):
-    arr = (dsa._PagePool * n)()
-    for a in arr:
-        a.data, a.page_bytes = data, page_bytes
-    return ctypes.addressof(arr), arr
 
 
 @pytest.mark.parametrize("call,word", [
@@ -56,6 +47,6 @@ def test_the_binding_refuses_other_shapes_and_host_tensors():
     with pytest.raises(ValueError):
         dsa.pages_release(ref, table, one, one)
     with pytest.raises(ValueError):
-        dsa._page_pools([torch.zeros((4, 16))], 4)
+        dsa.pages_compact(ref, table, [torch.zeros((4, 16))])
     with pytest.raises(ValueError):
-        dsa._page_pools([torch.zeros((4, 16))] * 9, 4)
+        dsa.pages_fork(ref, table, one, one, one, [])
