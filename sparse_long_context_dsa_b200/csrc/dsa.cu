@@ -1448,17 +1448,13 @@ dsa_status_t dsa_pages_release(const int32_t *ref_in, int32_t *ref_out, int64_t 
     int sms = 0;
     if ((st = device_info(sms)) != DSA_OK) return st;
     const int64_t table_n = (int64_t)n_req * max_pages;
-    if (ref_out != ref_in || table_out != table_in) {
-        const int64_t want = (n_pages + table_n + 4 * dsa::pages::kThreads - 1) / (4 * dsa::pages::kThreads);
-        if ((st = launch_k("copy_tables_kernel", dsa::pages::copy_tables_kernel,
-                           dim3((unsigned)std::min<int64_t>(want, 4 * sms)), dim3(dsa::pages::kThreads), 0, stream, 0,
-                           ref_in, ref_out, n_pages, table_in, table_out, table_n)) != DSA_OK)
-            return st;
-    }
-    if (n == 0) return DSA_OK;
-    const int ctas = std::max(1, std::min((max_pages + dsa::pages::kThreads - 1) / dsa::pages::kThreads, 8 * sms / n));
-    return launch_k("release_kernel", dsa::pages::release_kernel, dim3((unsigned)ctas, (unsigned)n),
-                    dim3(dsa::pages::kThreads), 0, stream, 0, ref_out, n_pages, table_out, max_pages, n_req, req, keep, n);
+    if (n == 0 && ref_out == ref_in && table_out == table_in) return DSA_OK;
+    // one cluster of up to 8 CTAs, a warp for every 32 entries to look at or copy
+    const int64_t work = (n_pages + table_n) / 4 + (int64_t)n * max_pages;
+    int size = 1;
+    while (size < 8 && size * 4 * (int64_t)dsa::pages::kScanThreads < work) size *= 2;
+    return launch_k("release_kernel", dsa::pages::release_kernel, dim3((unsigned)size), dim3(dsa::pages::kScanThreads), 0,
+                    stream, (unsigned)size, ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req, req, keep, n);
 }
 
 size_t dsa_pages_compact_workspace_size(int64_t n_pages)

@@ -181,8 +181,9 @@ __device__ __forceinline__ void copy_segment(const Pools &p, int seg, int64_t sr
         if (threadIdx.x + u * kThreads < n) d[threadIdx.x + u * kThreads] = v[u];
 }
 
-// One block row of the grid per fork; its CTAs share the copied page's segments, the first one
-// also writes the child's table row and the counts.
+// One block row of the grid per fork; its CTAs share the copied page's segments and the child's
+// table row with its counts (every entry is a chain of three dependent accesses: 939 entries in
+// one CTA held a call of 64 forks up for 6 of its 12.7 us).
 __global__ void __launch_bounds__(kThreads) fork_kernel(int32_t *ref_out, int64_t n_pages,
                                                         const int32_t *table_in, int32_t *table_out, int max_pages,
                                                         int n_req, const int32_t *parent, const int32_t *child,
@@ -230,8 +231,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(int32_t *ref_out, int64_
     }
     if (dst >= 0)
         for (int seg = blockIdx.x; seg < pools.first[pools.n]; seg += gridDim.x) copy_segment(pools, seg, src, dst);
-    if (blockIdx.x != 0) return;
-    for (int v = tid; v < max_pages; v += kThreads) {
+    for (int v = blockIdx.x * kThreads + tid; v < max_pages; v += gridDim.x * kThreads) {
         int page = -1;
         if (v < full) {
             page = from[v];
@@ -250,36 +250,49 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(int32_t *ref_out, int64_
     }
 }
 
-// Row req[i] cut to its first keep[i] tokens: its further pages are given back.
-__global__ void __launch_bounds__(kThreads) release_kernel(int32_t *ref, int64_t n_pages, int32_t *table, int max_pages,
-                                                           int n_req, const int32_t *req, const int32_t *keep, int n)
+// Rows req[i] cut to their first keep[i] tokens: their further pages are given back.  One cluster:
+// it copies the inputs where the outputs are other arrays, meets, and walks the listed rows.
+__global__ void __launch_bounds__(kScanThreads) release_kernel(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages,
+                                                               const int32_t *table_in, int32_t *table_out,
+                                                               int max_pages, int n_req, const int32_t *req,
+                                                               const int32_t *keep, int n)
 {
     pdl_trigger();   // the next kernel may launch; it waits for this one itself
     pdl_wait();      // the previous kernel's results are visible from here on
-    const int i = blockIdx.y, tid = threadIdx.x;
-    const int b = req[i], K = keep[i];
-    int twice = 0;
-    for (int j = tid; j < i; j += kThreads) twice |= req[j] == b;
-    twice = __syncthreads_or(twice);
-    if (twice || b < 0 || b >= n_req || K < 0) {
-        if (blockIdx.x == 0 && tid == 0) set_error(kErrPages);
-        return;
-    }
-    for (int64_t v = (K + (int64_t)kPage - 1) / kPage + blockIdx.x * kThreads + tid; v < max_pages; v += gridDim.x * kThreads) {
-        int32_t *e = table + (int64_t)b * max_pages + v;
-        const int page = *e;
+    const int64_t t = (int64_t)blockIdx.x * kScanThreads + threadIdx.x, nt = (int64_t)gridDim.x * kScanThreads;
+    if (ref_out != ref_in)
+        for (int64_t i = t; i < n_pages; i += nt) ref_out[i] = ref_in[i];
+    if (table_out != table_in)
+        for (int64_t i = t; i < (int64_t)n_req * max_pages; i += nt) table_out[i] = table_in[i];
+    __threadfence();
+    cg::this_cluster().sync();
+    // warps take the listed rows in pieces of 32 entries
+    const int lane = threadIdx.x & 31;
+    const int64_t pieces = (max_pages + 31) / 32;
+    for (int64_t w = t >> 5; w < n * pieces; w += nt >> 5) {
+        const int i = (int)(w / pieces), v = (int)(w % pieces) * 32 + lane;
+        const int b = req[i], K = keep[i];
+        bool twice = false;
+        for (int j = lane; j < i; j += 32) twice |= req[j] == b;
+        if (__any_sync(0xffffffffu, twice) || b < 0 || b >= n_req || K < 0) {
+            if (v == 0) set_error(kErrPages);
+            continue;
+        }
+        if (v >= max_pages || v < (K + (int64_t)kPage - 1) / kPage) continue;
+        int32_t *e = table_out + (int64_t)b * max_pages + v;
+        const int page = __ldcg(e);
         if (page == -1) continue;
         *e = -1;
         if (page < 0 || page >= n_pages) {
             set_error(kErrPages);
-        } else if (atomicSub(ref + page, 1) <= 0) {        // was free already
-            atomicAdd(ref + page, 1);
+        } else if (atomicSub(ref_out + page, 1) <= 0) {    // was free already
+            atomicAdd(ref_out + page, 1);
             set_error(kErrPages);
         }
     }
 }
 
-// Copies of the inputs of a release whose outputs are other arrays.
+// Copies of the inputs of a call that changes nothing, where its outputs are other arrays.
 __global__ void __launch_bounds__(kThreads) copy_tables_kernel(const int32_t *ref_in, int32_t *ref_out, int64_t n_pages,
                                                                const int32_t *table_in, int32_t *table_out, int64_t n)
 {
