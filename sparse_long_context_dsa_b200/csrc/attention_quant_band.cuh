@@ -1,0 +1,490 @@
+// Window GQA of many queries of a request over the 8-bit paged cache (layout and scales:
+// append_quant.cuh): neighbouring queries' windows are almost the same tokens.
+//
+// A CTA takes 8 queries of the list and one KV group: 128 rows (query, head), the MMA's M.  It
+// handles them in runs: queries of one request whose positions lie within 56 of one another share
+// one stream of their windows' pages (64 tokens, one TMA box of 24 KiB, a ring of 4); rows of the
+// other runs are masked.  A prefill chunk's 8 queries are one run.
+//  * S = q K^T: tcgen05.mma kind::f8f6f4 straight from the codes (K-major, 64-byte swizzle), q as
+//    two e4m3 terms of 2^-e q that accumulate into the same S (the second is off by at most 2^-18
+//    of the head's largest element);
+//  * softmax: thread = row (TMEM lane), fp32, log2 units, no exchange between threads.  As in the
+//    row kernel, the sum l has a reference m and the weights P' = 2^(s - m) sV 2^(m - M) one of
+//    their own, both moved only when a tile passes them by 2^10 (O is then rescaled in TMEM);
+//  * O += P' V: P' as three e5m2 terms (cut off, cut off, rounded: 2^-9 relative, ending at 2^-22
+//    of a row's largest) in shared memory, V's codes MN-major, N = 192.
+// V rows that no query of the run attends are zeroed in shared memory.  A NaN code at a token that
+// only some of them attend would reach the others (their P' is 0, but 0 * NaN is not): such
+// tokens are looked at, and a run that has one is done again, query by query.
+// Bound: the tensor pipe's instruction rate, 12 + 6 instructions per 64 tokens and 8 queries.
+#pragma once
+
+#include "attention_quant_tc.cuh"
+
+namespace dsa {
+namespace attnqb {
+
+using attnq::ex2;
+using attnq::kRegBytes;
+using attnq::Params;
+using attnqt::desc_hi;
+using attnqt::desc_lo;
+using attnqt::hsub2;
+using attnqt::mma_f8;
+
+constexpr int kQueries = 8;
+constexpr int kTileBytes = quant::kRegionsPerPage * kRegBytes;   // a page of one group: 24 KiB
+constexpr int kStages = 4;
+constexpr int kThreads = 192;                                    // warps 0-3 softmax, 4 MMA, 5 loads
+constexpr int kSpan = 56;                                        // positions of a run lie this close to its first
+constexpr int kOCol = 128;                                       // TMEM: S 0, 64; O 128 .. 319
+constexpr int kTmemCols = 512;
+constexpr float kBase = 5.0f;                                    // log2 of a weight at its reference
+constexpr float kSlack = 10.0f;                                  // log2 units a reference may lag behind
+
+struct Smem {
+    uint8_t q[2][3 * 128 * 64];                                  // hi, lo: [64-dim block][row][64], 64-byte swizzle
+    uint8_t p[2][3][128 * 64];                                   // [buffer][term][row][64 tokens], 64-byte swizzle
+    float4 scale[kStages][8];                                    // K's, V's, log2 of V's
+    int there[kStages];                                          // the page is there
+    float qscale[128];
+    int pos[kQueries], req[kQueries];
+    int run_end[kQueries];                                       // first query behind the run that begins here
+    int nan[2];                                                  // run n (by parity) met a NaN code at a partly attended token: n + 1
+    uint64_t full[kStages], empty[kStages], s_full[2], p_ready[2], pv_done[2], run_done, drain;
+    uint32_t tmem;
+};
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+
+constexpr uint32_t kIdescS = umma_idesc_e4m3(128, kPage);
+constexpr uint32_t kIdescO = umma_idesc_e4m3(128, kD) | (1u << 7) | (1u << 16);    // P' e5m2 K-major, V MN-major
+
+// The next run of a CTA's queries: [u0, u1), request b, tokens lo .. hi of its windows.
+struct Run {
+    int u0, u1, b, lo, hi, tiles;
+};
+
+__device__ __forceinline__ Run run_at(const Smem &sm, const Params &p, int u0, bool single)
+{
+    Run r;
+    r.u0 = u0;
+    r.u1 = single ? u0 + 1 : sm.run_end[u0];
+    r.b = sm.req[u0];
+    r.lo = INT_MAX;
+    r.hi = -1;
+    for (int u = u0; u < r.u1; ++u) {
+        r.lo = min(r.lo, max(0, sm.pos[u] - p.window + 1));
+        r.hi = max(r.hi, sm.pos[u]);
+    }
+    r.tiles = r.hi < 0 ? 0 : r.hi / kPage - r.lo / kPage + 1;
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_attn_band_kernel(const __grid_constant__ CUtensorMap tmap, const Params p)
+{
+    pdl_trigger();   // the next kernel may launch; it waits for this one itself
+    if (threadIdx.x == 0) prefetch_tensormap(&tmap);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem &sm = *reinterpret_cast<Smem *>(ring + kStages * kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.full[i], 2);                           // the load is announced; the scales are there
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_ready[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+        }
+        mbar_init(&sm.run_done, 6);                              // every role: none is two runs behind another
+        mbar_init(&sm.drain, 1);
+        sm.nan[0] = sm.nan[1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) tmem_alloc(&sm.tmem, kTmemCols);
+    pdl_wait();      // the previous kernel's results are visible from here on
+    const int blocks = (p.nq + kQueries - 1) / kQueries;
+    const int g = (int)blockIdx.x / blocks, q0 = ((int)blockIdx.x % blocks) * kQueries;
+    const int n_q = min(kQueries, p.nq - q0);
+    if (tid < kQueries) {
+        int pos = -1, req = -1;
+        if (tid < n_q) {
+            pos = p.q_pos[q0 + tid];
+            req = p.q_req ? p.q_req[q0 + tid] : q0 + tid;
+            if (pos >= 0 && (req < 0 || req >= p.n_req)) {
+                set_error(kErrAttnIndex);
+                pos = -1;
+            }
+        }
+        sm.pos[tid] = pos;                                       // -1: attends nothing
+        sm.req[tid] = req;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid < kQueries) {
+        const int p0 = sm.pos[tid];
+        int e = tid + 1;
+        while (p0 >= 0 && e < kQueries && sm.pos[e] >= 0 && sm.req[e] == sm.req[tid] && abs(sm.pos[e] - p0) <= kSpan) ++e;
+        sm.run_end[tid] = e;
+    }
+    const uint32_t tmem = sm.tmem;
+    // q of every query: 2^-e q = hi + lo in e4m3; 8 threads share a head, thread c of them holds dims
+    // 8 c .. 8 c + 7 of every 64-dim block
+    if (warp < 4) {
+        const int h = tid >> 3, c = tid & 7;
+#pragma unroll 2
+        for (int u = 0; u < n_q; ++u) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((int64_t)(q0 + u) * kHQ + g * kHeadsPerGroup + h) * kD + 8 * c);
+            uint4 qv[3];
+            __nv_bfloat162 a2 = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                qv[j] = __ldg(src + 8 * j);
+                const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a2 = __hmax2(a2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+            }
+            float a = fmaxf(__low2float(a2), __high2float(a2));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+            const float s = quant::block_scale(a), inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            const int r = 16 * u + h;
+            if (c == 0) sm.qscale[r] = s * p.scale_log2;
+            const int at = r * 64 + ((((c >> 1) ^ ((r >> 1) & 3)) << 4) | ((c & 1) << 3));
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = bf16_lo(w[i]) * inv, y = bf16_hi(w[i]) * inv;
+                    hi[i] = cvt_e4m3x2(x, y);
+                    const uint32_t back = attnq::e4m3x2_to_f16x2((uint16_t)hi[i]);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                    lo[i] = cvt_e4m3x2(x - f.x, y - f.y);
+                }
+                *reinterpret_cast<uint2 *>(sm.q[0] + j * 8192 + at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                *reinterpret_cast<uint2 *>(sm.q[1] + j * 8192 + at) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            }
+        }
+        fence_proxy_async();
+    }
+    __syncthreads();                                             // q, the runs
+
+    // Every role walks the same runs: after a run that met a NaN (read behind the run's barrier), its
+    // queries one by one.
+    int n_run = 0, u0 = 0, single_until = 0;
+    bool ok = true;
+    auto next = [&](const Run &r) {                              // the run is done: where the next one begins
+        const int met = *reinterpret_cast<volatile int *>(&sm.nan[n_run & 1]);
+        ++n_run;
+        if (u0 >= single_until && r.u1 - r.u0 > 1 && met == n_run) {
+            single_until = r.u1;
+        } else {
+            u0 = r.u1;
+        }
+    };
+    int tg = 0;                                                  // tiles before this one, over all runs
+
+    if (warp == 5) {
+        // ---- loads: a page of the group at a time
+        while (u0 < n_q && ok) {
+            const Run r = run_at(sm, p, u0, u0 < single_until);
+            for (int ti = 0; ti < r.tiles; ++ti, ++tg) {
+                const int st = tg % kStages, v = r.lo / kPage + ti;
+                int page = -1;
+                if (v < p.max_pages) page = p.block_table[(int64_t)r.b * p.max_pages + v];
+                const bool there = page >= 0 && page < p.n_pages;
+                if (!there && lane == 0) set_error(kErrAttnIndex);
+                const int block = there ? (page * kG + g) * quant::kRegionsPerPage : 0;
+                // scales of regions that hold a token of the windows
+                const int tok = v * kPage + 8 * lane;
+                float2 sc = make_float2(0.0f, 0.0f);
+                if (there && lane < 8 && tok <= r.hi && tok + 7 >= r.lo) sc = __ldg(p.scale + block + lane);
+                if (tg >= kStages) ok = __all_sync(0xffffffffu, mbar_wait_sleep(&sm.empty[st], (unsigned)(tg / kStages - 1) & 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    if (there) {
+                        mbar_arrive_expect_tx(&sm.full[st], (unsigned)kTileBytes);
+                        attnqt::tma_load_4d(ring + st * kTileBytes, &tmap, 0, 0, 0, block, &sm.full[st]);
+                    } else {
+                        mbar_arrive(&sm.full[st]);
+                    }
+                    sm.there[st] = there;
+                }
+                if (lane < 8) sm.scale[st][lane] = make_float4(sc.x, sc.y, log2f(sc.y), 0.0f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[st]);
+            }
+            if (ok && lane == 0) mbar_arrive(&sm.run_done);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_sleep(&sm.run_done, (unsigned)n_run & 1u));
+            next(r);
+        }
+        // none of this warp's loads is in flight when the CTA ends, after a wait that gave up as well
+        __syncwarp();
+        if (lane == 0)
+            for (int s = 0; s < kStages && s < tg; ++s) {
+                const int last = tg - 1 - (tg - 1 - s) % kStages;
+                mbar_wait(&sm.full[s], (unsigned)(last / kStages) & 1u);
+            }
+        __syncwarp();
+    } else if (warp == 4) {
+        // ---- MMA issuer (one lane): S(i), then O += P'(i - 1) V(i - 1)
+        if (lane == 0) {
+            // K rows of 64 bytes, 8 of a region 512 bytes, regions 3 KiB apart; V^T: 64-dim blocks 1 KiB
+            // apart, 8-token groups 3 KiB apart; q and P': rows of 64 bytes
+            const uint32_t k_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring) + 512, 1024);
+            constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
+            int j = 0;                                           // P' V issued, over all runs
+            auto issue_pv = [&](bool fresh) {
+                ok = ok && mbar_wait(&sm.p_ready[j & 1], (unsigned)(j >> 1) & 1u);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t b = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4);
+#pragma unroll
+                for (int term = 0; term < 3; ++term) {
+                    const uint32_t a = desc_lo(smem_u32(sm.p[j & 1][term]), 16);
+                    if (term == 0 && fresh) mma_f8<false>(tmem + kOCol, a, kRowsHi, b, kKvHi, kIdescO);
+                    else mma_f8<true>(tmem + kOCol, a, kRowsHi, b, kKvHi, kIdescO);
+                    mma_f8<true>(tmem + kOCol, a + (32 >> 4), kRowsHi, b + (4 * kRegBytes >> 4), kKvHi, kIdescO);
+                }
+                umma_commit(&sm.empty[j % kStages]);
+                umma_commit(&sm.pv_done[j & 1]);
+                ++j;
+            };
+            while (u0 < n_q && ok) {
+                const Run r = run_at(sm, p, u0, u0 < single_until);
+                for (int ti = 0; ti < r.tiles && ok; ++ti, ++tg) {
+                    const int st = tg % kStages;
+                    ok = mbar_wait(&sm.full[st], (unsigned)(tg / kStages) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t b = k_lo + (uint32_t)st * (kTileBytes >> 4), d = tmem + 64 * (tg & 1);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int ks = 0; ks < 6; ++ks) {
+                            const uint32_t a = desc_lo(smem_u32(sm.q[term]) + (ks >> 1) * 8192 + (ks & 1) * 32, 16);
+                            const uint32_t bk = b + (((ks >> 1) * 1024 + (ks & 1) * 32) >> 4);
+                            if (term == 0 && ks == 0) mma_f8<false>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                            else mma_f8<true>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                        }
+                    umma_commit(&sm.s_full[tg & 1]);
+                    if (ti > 0) issue_pv(ti == 1);
+                }
+                if (r.tiles > 0) issue_pv(r.tiles == 1);
+                if (ok) mbar_arrive(&sm.run_done);
+                ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
+                next(r);
+            }
+            // no MMA is in flight when TMEM is released, after a wait that gave up as well
+            umma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0u);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = row 16 u + h
+        const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
+        const int u = tid >> 4;
+        const float qf = sm.qscale[tid];
+        const int64_t head = (int64_t)(q0 + u) * kHQ + g * kHeadsPerGroup + (tid & 15);
+        bool landed = true;
+        // a wait that gives up leaves the error flag and garbage; the later ones are then short
+        auto wait = [&](uint64_t *bar, unsigned parity) {
+            if (!mbar_wait(bar, parity, landed ? kWaitLimitCycles : 1ll << 22)) landed = false;
+        };
+        while (u0 < n_q) {
+            const Run r = run_at(sm, p, u0, u0 < single_until);
+            const bool mine = u >= r.u0 && u < r.u1;
+            const int pos = mine ? sm.pos[u] : -1, t_lo = mine ? max(0, pos - p.window + 1) : 0;
+            // tokens that every query of the run attends: all_lo .. all_hi
+            int all_lo = 0, all_hi = INT_MAX;
+            for (int i = r.u0; i < r.u1; ++i) {
+                all_lo = max(all_lo, max(0, sm.pos[i] - p.window + 1));
+                all_hi = min(all_hi, sm.pos[i]);
+            }
+            float m = -INFINITY, M = -INFINITY, mref = 0.0f, c = 0.0f, l = 0.0f;
+            for (int ti = 0; ti < r.tiles; ++ti, ++tg) {
+                const int st = tg % kStages, t0 = (r.lo / kPage + ti) * kPage;
+                wait(&sm.full[st], (unsigned)(tg / kStages) & 1u);
+                const bool there = sm.there[st] != 0;
+                const bool whole = there && t0 >= all_lo && t0 + kPage - 1 <= all_hi;
+                if (!whole && tid < kPage) {
+                    // V rows that nobody attends: zero; that some attend: looked at for NaN
+                    const int t = t0 + tid;
+                    const bool none = !there || t < r.lo || t > r.hi;
+                    if (none || t < all_lo || t > all_hi) {
+                        uint8_t *v = ring + st * kTileBytes + (tid >> 3) * kRegBytes + 512 + (tid & 7) * 64;
+                        bool bad = false;
+#pragma unroll 1
+                        for (int i = 0; i < 12; ++i) {
+                            uint4 *x = reinterpret_cast<uint4 *>(v + (i >> 2) * 1024 + (i & 3) * 16);
+                            if (none) {
+                                *x = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 y = *x;
+                                bad |= (__vcmpeq4(y.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(y.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                                        __vcmpeq4(y.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(y.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
+                            }
+                        }
+                        if (bad) sm.nan[n_run & 1] = n_run + 1;
+                    }
+                }
+                wait(&sm.s_full[tg & 1], (unsigned)(tg >> 1) & 1u);
+                __syncwarp();
+                tc_fence_after();
+                float s[64];
+                {
+                    float a[32], b[32];
+                    tmem_ld32x2(trow + 64 * (tg & 1), trow + 64 * (tg & 1) + 32, a, b);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        s[i] = a[i];
+                        s[32 + i] = b[i];
+                    }
+                }
+                tc_fence_before();
+                float mx = -INFINITY, mv = -INFINITY;
+                if (whole && __all_sync(0xffffffffu, mine)) {
+#pragma unroll
+                    for (int rg = 0; rg < 8; ++rg) {
+                        const float4 sc = sm.scale[st][rg];
+                        const float f = qf * sc.x;
+                        float y = -INFINITY;
+#pragma unroll
+                        for (int i = 8 * rg; i < 8 * rg + 8; ++i) {
+                            s[i] *= f;
+                            y = fmaxf(y, s[i]);
+                        }
+                        mx = fmaxf(mx, y);
+                        mv = fmaxf(mv, y + sc.z);
+                    }
+                } else {
+#pragma unroll
+                    for (int rg = 0; rg < 8; ++rg) {
+                        const float4 sc = sm.scale[st][rg];
+                        const float f = qf * sc.x;
+                        float y = -INFINITY;
+#pragma unroll
+                        for (int i = 8 * rg; i < 8 * rg + 8; ++i) {
+                            const int t = t0 + i;
+                            s[i] = there && t >= t_lo && t <= pos ? s[i] * f : -INFINITY;
+                            y = fmaxf(y, s[i]);
+                        }
+                        mx = fmaxf(mx, y);
+                        mv = fmaxf(mv, y + sc.z);
+                    }
+                }
+                // the references move where a token passes one by more than the slack, or there is none
+                const bool grow = mx > m + kSlack || mv > M + kSlack || (M == -INFINITY && mx > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    float al = 1.0f, ao = 1.0f;
+                    if (grow) {
+                        const float a = fmaxf(m, mx), d = fmaxf(M, mv);
+                        if (a != m) al = exp2f(m - a);
+                        if (d != M) ao = exp2f(M - d);
+                        m = a;
+                        M = d;
+                        mref = a == -INFINITY ? 0.0f : a - kBase;
+                        c = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
+                        l *= al;
+                    }
+                    if (ti > 0 && __any_sync(0xffffffffu, ao != 1.0f)) {
+                        // O holds the tiles before this one once their MMAs are done
+                        wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kD; c0 += 16) {
+                            float o[16];
+                            attnqt::tmem_ld16(trow + kOCol + c0, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= ao;
+                            attnqt::tmem_st16(trow + kOCol + c0, o);
+                        }
+                        tc_fence_before();
+                    }
+                }
+                // P' in three e5m2 terms: the upper bytes of w, of what they leave, and of the rest,
+                // rounded; 16 tokens at a time
+                uint8_t *dst = sm.p[tg & 1][0] + tid * 64;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float f = fminf(sm.scale[st][2 * ch + hf].y * c, 8.5070592e37f);     // 2^126
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 16 * ch + 8 * hf + 2 * i;
+                            const float p0 = ex2(s[e] - mref), p1 = ex2(s[e + 1] - mref);
+                            l += p0 + p1;
+                            w[4 * hf + i] = attnq::pack_f16x2(p0 * f, p1 * f);
+                        }
+                    }
+                    const int at = (ch ^ ((tid >> 1) & 3)) << 4;
+#pragma unroll
+                    for (int term = 0; term < 3; ++term) {
+                        if (term == 2) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] += 0x00800080u;
+                        }
+                        *reinterpret_cast<uint4 *>(dst + term * (128 * 64) + at) =
+                            make_uint4(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531),
+                                       __byte_perm(w[4], w[5], 0x7531), __byte_perm(w[6], w[7], 0x7531));
+                        if (term < 2) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = hsub2(w[i], w[i] & 0xFF00FF00u);
+                        }
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[tg & 1]);
+            }
+            // ---- the run's rows
+            if (r.tiles > 0) wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
+            __syncwarp();
+            tc_fence_after();
+            // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
+            const float f = l > 0.0f ? (M > -INFINITY ? exp2f(M - m) / l : 0.0f) : l;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kD; c0 += 16) {
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+                if (r.tiles > 0) attnqt::tmem_ld16(trow + kOCol + c0, o);
+                if (mine) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
+                    uint2 *dst = reinterpret_cast<uint2 *>(p.out + head * kD + c0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dst[i] = make_uint2(y[2 * i], y[2 * i + 1]);
+                }
+            }
+            if (mine && p.lse) p.lse[head] = l == 0.0f ? -INFINITY : (m - kBase + log2f(l)) * 0.69314718055994531f;
+            tc_fence_before();
+            // every warp has looked at the run's tokens (sm.nan) before any role goes on
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.run_done);
+            wait(&sm.run_done, (unsigned)n_run & 1u);
+            __syncwarp();
+            next(r);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();                                             // every role is done (or gave up)
+    tc_fence_after();
+    if (warp == 4) tmem_free(tmem, kTmemCols);
+}
+
+}  // namespace attnqb
+}  // namespace dsa

@@ -14,6 +14,7 @@
 #include "attention.cuh"
 #include "attention_cluster.cuh"
 #include "attention_quant.cuh"
+#include "attention_quant_band.cuh"
 #include "attention_quant_tc.cuh"
 #include "attention_tc.cuh"
 #include "common.cuh"
@@ -108,6 +109,7 @@ dsa_status_t group_range_args(int g0, int ng)
 }
 
 constexpr int kGemmMinQueries = 64;   // FP8 prefill chunks at least this long use the GEMM
+constexpr int kBandMinQueries = 32;   // quantised window calls at least this long share neighbours' windows
 constexpr int kSharedMinQueries = 32; // prefill attention calls at least this long share selections
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1203,7 +1205,10 @@ dsa_status_t attn_quant_attributes()
     return attr.once([] {
         const auto fn = dsa::attnqt::sparse_attn_quant_tc_kernel;
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsa::attnqt::kSmemBytes);
-        return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        const cudaError_t b = cudaFuncSetAttribute(dsa::attnqb::window_attn_band_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)dsa::attnqb::kSmemBytes);
+        return b != cudaSuccess ? b : cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
 }
 
@@ -1257,6 +1262,19 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     p.k = k;
     p.window = window;
     p.scale_log2 = dsa::attnq::kLog2e / sqrtf((float)dsa::kD);
+    // chunks: 8 neighbouring queries of the list share their windows' tokens where a request has at
+    // least that many queries on average
+    if (window > 0 && nq >= kBandMinQueries && nq >= 8 * (int64_t)n_req) {
+        const cuuint64_t dims[4] = {64, 16, 3, (cuuint64_t)n_pages * dsa::kG * (dsa::kPage / dsa::kRegion)};
+        const cuuint64_t strides[3] = {(cuuint64_t)dsa::kD, 64, (cuuint64_t)dsa::quant::kRegionBytesQ};
+        const cuuint32_t box[4] = {64, 16, 3, (cuuint32_t)(dsa::kPage / dsa::kRegion)};       // a group's page
+        if ((st = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kv_cache, dims, strides, box,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_64B)) != DSA_OK)
+            return st;
+        const int blocks = (nq + dsa::attnqb::kQueries - 1) / dsa::attnqb::kQueries * dsa::kG;
+        return launch_k("window_attn_band_kernel", dsa::attnqb::window_attn_band_kernel, dim3((unsigned)blocks),
+                        dim3(dsa::attnqb::kThreads), dsa::attnqb::kSmemBytes, stream, 0, map, p);
+    }
     // CTAs per row: as many as fit the GPU at once, while each keeps half a tile of regions
     const int64_t rows = (int64_t)nq * dsa::kG;
     const int most = window > 0 ? window_regions(window) : k;

@@ -163,6 +163,78 @@ def test_window_chunk_of_one_request():
     Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 150, pos, Q.window_tokens(pos, 512)))
 
 
+@pytest.mark.parametrize("w", [1, 9, 64, 100, 512])
+def test_window_chunks_of_several_requests(w):
+    # lists whose neighbours share windows, or do not: two requests' chunks one behind the other
+    # (ends inside a block of 8), far positions, a descending stretch, the same position twice, padding
+    pages = 30
+    table = Q.random_table([900, 400], pages, w)
+    cache, scale = Q.filled_cache(pages, w + 1)
+    pos = list(range(20)) + list(range(700, 741)) + list(range(260, 300)) + [5, 890, 5, 890, 300, 299, 298, 297, 64, 64, -1, 64, -1, -1, 399]
+    req = [0] * 61 + [1] * 40 + [0, 0, 1, 0, 1, 1, 1, 1, 0, 0, 0, 0, 1, 1, 1]
+    q = Q.rows((len(pos), 64, 192), w + 2, 0.3)
+    out, lse = window(cache, scale, table, q, req, pos, w)
+    ref = reference(cache, scale, table, q, req, pos, Q.window_tokens(pos, w))
+    Q.check_attention(out, lse, ref)
+    for i, p in enumerate(pos):
+        if p < 0:
+            assert not out[i].any() and torch.isinf(lse[i]).all()
+
+
+def test_nan_at_a_token_that_some_of_a_chunk_attend():
+    # V of two tokens: the newest one (the last query alone attends it) and the oldest of the first
+    # query's window; the rest of the 8 stay finite
+    pages = 14
+    table = Q.random_table([800], pages, 130)
+    cache, scale = Q.filled_cache(pages, 131)
+    pos = list(range(704, 744))
+    q = Q.rows((40, 64, 192), 132, 0.3)
+    clean, _ = window(cache, scale, table, q, [0] * 40, pos, 512)
+    for t, dim in ((743, 3), (704 - 511, 5)):
+        cache[table[0, t // 64], :, t % 64 // 8, 1, t % 8, dim] = 0x7F
+    out, lse = window(cache, scale, table, q, [0] * 40, pos, 512)
+    nan = torch.isnan(out)
+    assert nan[39, :, 3].all() and nan[0, :, 5].all() and int(nan.sum()) == 2 * 64
+    out[39, :, 3] = clean[39, :, 3]
+    out[0, :, 5] = clean[0, :, 5]
+    # the others: the two tokens' own other dims are as they were, so nothing else has changed but the
+    # order in which references move; both are within the tolerance of the same 64-bit rows
+    cache = cache.clone()
+    for t, dim in ((743, 3), (704 - 511, 5)):
+        cache[table[0, t // 64], :, t % 64 // 8, 1, t % 8, dim] = 0
+    ref = list(reference(cache, scale, table, q, [0] * 40, pos, Q.window_tokens(pos, 512)))
+    for i, dim in ((39, 3), (0, 5)):
+        ref[0][i, :, dim] = out[i, :, dim].double().cpu().numpy()
+    Q.check_attention(out, lse, ref)
+
+
+def test_bad_pages_and_requests_in_a_chunk():
+    pages = 10
+    table = Q.random_table([500], pages, 133)
+    cache, scale = Q.filled_cache(pages, 134)
+    pos = list(range(450, 490))
+    req = [0] * 40
+    q = Q.rows((40, 64, 192), 135, 0.3)
+    bad = table.copy()
+    bad[0, 5] = pages                                              # tokens 320 .. 383
+    out, lse = window(cache, scale, bad, q, req, pos, 200, check=False)
+    with pytest.raises(dsa.DsaError):
+        dsa.check_device()
+    tok = Q.window_tokens(pos, 200)
+    Q.check_attention(out, lse, reference(cache, scale, table, q, req, pos,
+                                          lambda i, g: tok(i, g)[tok(i, g) // 64 != 5]))
+    req[11] = 1                                                    # no such request: that query alone
+    out, lse = window(cache, scale, table, q, req, pos, 200, check=False)
+    with pytest.raises(dsa.DsaError):
+        dsa.check_device()
+    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 40, pos,
+                                          lambda i, g: tok(i, g)[:0] if i == 11 else tok(i, g)))
+    out, lse = window(cache, scale, table[:, :7], q, [0] * 40, pos, 200, check=False)       # the table ends at token 447
+    with pytest.raises(dsa.DsaError):
+        dsa.check_device()
+    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 40, pos, lambda i, g: tok(i, g)[tok(i, g) < 448]))
+
+
 def test_window_over_a_ring():
     ring = 9
     table = (np.arange(2)[:, None] * ring + np.arange(2000)[None] % ring).astype(np.int32)
