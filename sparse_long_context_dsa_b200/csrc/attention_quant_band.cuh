@@ -3,7 +3,7 @@
 //
 // A CTA takes 8 queries of the list and one KV group: 128 rows (query, head), the MMA's M.  It
 // handles them in runs: queries of one request whose positions lie within 56 of one another share
-// one stream of their windows' pages (64 tokens, one TMA box of 24 KiB, a ring of 4); rows of the
+// one stream of their windows' pages (64 tokens, 24 KiB, a ring of 4); rows of the
 // other runs are masked.  A prefill chunk's 8 queries are one run.
 //  * S = q K^T: tcgen05.mma kind::f8f6f4 straight from the codes (K-major, 64-byte swizzle), q as
 //    two e4m3 terms of 2^-e q that accumulate into the same S (the second is off by at most 2^-18
@@ -59,6 +59,19 @@ static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 
 constexpr uint32_t kIdescS = umma_idesc_e4m3(128, kPage);
 constexpr uint32_t kIdescO = umma_idesc_e4m3(128, kD) | (1u << 7) | (1u << 16);    // P' e5m2 K-major, V MN-major
+
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes written from registers (not waited for).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+          "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+          "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
+          "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
 
 // The next run of a CTA's queries: [u0, u1), request b, tokens lo .. hi of its windows.
 struct Run {
@@ -137,15 +150,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 8 c .. 8 c + 7 of every 64-dim block
     if (warp < 4) {
         const int h = tid >> 3, c = tid & 7;
-#pragma unroll 2
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((int64_t)q0 * kHQ + g * kHeadsPerGroup + h) * kD + 8 * c);
+        constexpr int kNext = kHQ * kD / 8;                      // 16-byte pieces from one query to the next
+        uint4 ahead[2][3];                                       // the next two queries' pieces, in flight
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) ahead[u][j] = u < n_q ? __ldg(src + u * kNext + 8 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
         for (int u = 0; u < n_q; ++u) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + ((int64_t)(q0 + u) * kHQ + g * kHeadsPerGroup + h) * kD + 8 * c);
             uint4 qv[3];
             __nv_bfloat162 a2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
-                qv[j] = __ldg(src + 8 * j);
+                qv[j] = ahead[0][j];
+                ahead[0][j] = ahead[1][j];
+                if (u + 2 < n_q) ahead[1][j] = __ldg(src + (u + 2) * kNext + 8 * j);
                 const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a2 = __hmax2(a2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
@@ -204,21 +224,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool there = page >= 0 && page < p.n_pages;
                 if (!there && lane == 0) set_error(kErrAttnIndex);
                 const int block = there ? (page * kG + g) * quant::kRegionsPerPage : 0;
-                // scales of regions that hold a token of the windows
+                // the regions that hold a token of the windows (lane l: region l), each in a box of its
+                // own: one box of the page's 8 takes 6,000 cycles to land, 8 boxes 1,600
                 const int tok = v * kPage + 8 * lane;
-                float2 sc = make_float2(0.0f, 0.0f);
-                if (there && lane < 8 && tok <= r.hi && tok + 7 >= r.lo) sc = __ldg(p.scale + block + lane);
+                const bool held = there && lane < 8 && tok <= r.hi && tok + 7 >= r.lo;
+                const unsigned boxes = __popc(__ballot_sync(0xffffffffu, held));
+                const float2 sc = held ? __ldg(p.scale + block + lane) : make_float2(0.0f, 0.0f);
                 if (tg >= kStages) ok = __all_sync(0xffffffffu, mbar_wait_sleep(&sm.empty[st], (unsigned)(tg / kStages - 1) & 1u));
                 if (!ok) break;
                 if (lane == 0) {
-                    if (there) {
-                        mbar_arrive_expect_tx(&sm.full[st], (unsigned)kTileBytes);
-                        attnqt::tma_load_4d(ring + st * kTileBytes, &tmap, 0, 0, 0, block, &sm.full[st]);
-                    } else {
-                        mbar_arrive(&sm.full[st]);
-                    }
+                    if (boxes) mbar_arrive_expect_tx(&sm.full[st], boxes * kRegBytes);
+                    else mbar_arrive(&sm.full[st]);
                     sm.there[st] = there;
                 }
+                __syncwarp();
+                if (held) tma_load_3d(ring + st * kTileBytes + lane * kRegBytes, &tmap, 0, (block + lane) * 16, 0, &sm.full[st]);
                 if (lane < 8) sm.scale[st][lane] = make_float4(sc.x, sc.y, log2f(sc.y), 0.0f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[st]);
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (none || t < all_lo || t > all_hi) {
                         uint8_t *v = ring + st * kTileBytes + (tid >> 3) * kRegBytes + 512 + (tid & 7) * 64;
                         bool bad = false;
-#pragma unroll 1
+#pragma unroll 4
                         for (int i = 0; i < 12; ++i) {
                             uint4 *x = reinterpret_cast<uint4 *>(v + (i >> 2) * 1024 + (i & 3) * 16);
                             if (none) {
@@ -402,13 +422,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kD; c0 += 16) {
-                            float o[16];
-                            attnqt::tmem_ld16(trow + kOCol + c0, o);
+                        for (int c0 = 0; c0 < kD; c0 += 64) {
+                            float o[32], o2[32];
+                            tmem_ld32x2(trow + kOCol + c0, trow + kOCol + c0 + 32, o, o2);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= ao;
-                            attnqt::tmem_st16(trow + kOCol + c0, o);
+                            for (int i = 0; i < 32; ++i) {
+                                o[i] *= ao;
+                                o2[i] *= ao;
+                            }
+                            tmem_st32(trow + kOCol + c0, o);
+                            tmem_st32(trow + kOCol + c0 + 32, o2);
                         }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tc_fence_before();
                     }
                 }
@@ -455,23 +480,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
             const float f = l > 0.0f ? (M > -INFINITY ? exp2f(M - m) / l : 0.0f) : l;
+            // through shared memory (this warp's share of the P' tiles, which its last MMAs have read), so
+            // that a warp writes whole rows of the output: 32 rows of 384 B, 16-byte pieces XORed by the row
+            uint8_t *rows = sm.p[0][0] + warp * (32 * 2 * kD);
 #pragma unroll 1
-            for (int c0 = 0; c0 < kD; c0 += 16) {
-                float o[16];
+            for (int c0 = 0; c0 < kD; c0 += 32) {
+                float o[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-                if (r.tiles > 0) attnqt::tmem_ld16(trow + kOCol + c0, o);
-                if (mine) {
-                    uint32_t y[8];
+                for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+                if (r.tiles > 0) tmem_ld32(trow + kOCol + c0, o);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
-                    uint2 *dst = reinterpret_cast<uint2 *>(p.out + head * kD + c0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dst[i] = make_uint2(y[2 * i], y[2 * i + 1]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(rows + lane * (2 * kD) + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                                   pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
             }
+            __syncwarp();
+            // (out is 8-byte aligned: two stores of 8 bytes where it is not 16-byte aligned)
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+            int row = lane / 24, piece = lane % 24;              // 24 pieces of 16 bytes a row, 32 at a time
+#pragma unroll 8
+            for (int i = 0; i < 24; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(rows + row * (2 * kD) + ((piece ^ (row & 7)) << 4));
+                const int v = 2 * warp + (row >> 4);
+                __nv_bfloat16 *dst = p.out + ((int64_t)(q0 + v) * kHQ + g * kHeadsPerGroup + (row & 15)) * kD + 8 * piece;
+                if (v >= r.u0 && v < r.u1) {
+                    if (wide) {
+                        *reinterpret_cast<uint4 *>(dst) = x;
+                    } else {
+                        reinterpret_cast<uint2 *>(dst)[0] = make_uint2(x.x, x.y);
+                        reinterpret_cast<uint2 *>(dst)[1] = make_uint2(x.z, x.w);
+                    }
+                }
+                piece += 8;
+                row += piece >= 24 ? 2 : 1;
+                piece -= piece >= 24 ? 24 : 0;
+            }
+            __syncwarp();
             if (mine && p.lse) p.lse[head] = l == 0.0f ? -INFINITY : (m - kBase + log2f(l)) * 0.69314718055994531f;
             tc_fence_before();
+            fence_proxy_async();
             // every warp has looked at the run's tokens (sm.nan) before any role goes on
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.run_done);

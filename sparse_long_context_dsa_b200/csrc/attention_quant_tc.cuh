@@ -88,15 +88,6 @@ __device__ __forceinline__ bool any_above_top(uint32_t v)
     return __hgt2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0x7800))) != 0u;
 }
 
-__device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                            uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(smem_u32(smem_dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // 16 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per lane).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
 {

@@ -1265,12 +1265,6 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     // chunks: 8 neighbouring queries of the list share their windows' tokens where a request has at
     // least that many queries on average
     if (window > 0 && nq >= kBandMinQueries && nq >= 8 * (int64_t)n_req) {
-        const cuuint64_t dims[4] = {64, 16, 3, (cuuint64_t)n_pages * dsa::kG * (dsa::kPage / dsa::kRegion)};
-        const cuuint64_t strides[3] = {(cuuint64_t)dsa::kD, 64, (cuuint64_t)dsa::quant::kRegionBytesQ};
-        const cuuint32_t box[4] = {64, 16, 3, (cuuint32_t)(dsa::kPage / dsa::kRegion)};       // a group's page
-        if ((st = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kv_cache, dims, strides, box,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_64B)) != DSA_OK)
-            return st;
         const int blocks = (nq + dsa::attnqb::kQueries - 1) / dsa::attnqb::kQueries * dsa::kG;
         return launch_k("window_attn_band_kernel", dsa::attnqb::window_attn_band_kernel, dim3((unsigned)blocks),
                         dim3(dsa::attnqb::kThreads), dsa::attnqb::kSmemBytes, stream, 0, map, p);
