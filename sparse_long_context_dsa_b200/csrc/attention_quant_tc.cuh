@@ -296,15 +296,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             int i_s = 0, i_p = 0, i = 0, j = 0;
             int n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
             int reg_p = r_p < rows ? row_of(p, r_p, rank, false).n_reg : 0;
-            bool ok = true;
+            bool ok = true, have_q = false;
             long long since = clock64();
             while (ok) {
-                // rows without (further) tiles
-                while (r_s < rows && i_s == n_s) {
+                // the q of every row is waited for in turn, that of a row without tiles too (a barrier's
+                // parity tells a phase from the next, not from the one after that)
+                if (!have_q && r_s < rows) have_q = mbar_test(&sm.q_ready, rows_s & 1u);
+                if (have_q && i_s == n_s) {
                     r_s += step;
                     ++rows_s;
                     i_s = 0;
                     n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
+                    have_q = false;
                 }
                 while (r_p < rows && i_p * kTileRegions >= reg_p) {
                     r_p += step;
@@ -331,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     ++j;
                     ++i_p;
                     since = clock64();
-                } else if (r_s < rows && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u) &&
-                           (i_s > 0 || mbar_test(&sm.q_ready, rows_s & 1u))) {
+                } else if (have_q && i_s < n_s && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u)) {
                     tc_fence_after();
                     const uint32_t a = k_lo + (uint32_t)(i % kStages) * (kTileBytes >> 4), d = tmem + 32 * (i & 1);
                     mma_f8<false>(d, a, kKvHi, q_lo, kQHi, kIdescS);

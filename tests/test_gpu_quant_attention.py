@@ -157,10 +157,28 @@ def test_window_chunk_of_one_request():
     pages = 12
     table = Q.random_table([700], pages, 93)
     cache, scale = Q.filled_cache(pages, 94)
-    pos = list(range(550, 700))
-    q = Q.rows((150, 64, 192), 95, 0.3)
-    out, lse = window(cache, scale, table, q, [0] * 150, pos, 512)
-    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 150, pos, Q.window_tokens(pos, 512)))
+    for n in (150, 203):                                            # row by row; shared
+        pos = list(range(700 - n, 700))
+        q = Q.rows((n, 64, 192), 95, 0.3)
+        out, lse = window(cache, scale, table, q, [0] * n, pos, 512)
+        Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * n, pos, Q.window_tokens(pos, 512)))
+
+
+def test_window_chunk_into_an_output_of_eight_byte_alignment():
+    # (the C call takes it; 16-byte stores would fault or split rows)
+    pages, n, w = 6, 200, 100
+    table = Q.random_table([300], pages, 136)
+    cache, scale = Q.filled_cache(pages, 137)
+    pos = list(range(100, 300))
+    q = Q.rows((n, 64, 192), 138, 0.3)
+    want, _ = window(cache, scale, table, q, [0] * n, pos, w)
+    raw = torch.zeros(n * 64 * 192 + 4, dtype=torch.bfloat16, device="cuda")
+    c, s, bt, p, r, qq = cache.cuda(), scale.cuda(), to(table), to(pos), to([0] * n), q.cuda()
+    st = dsa.lib().dsa_window_attn_quant(qq.data_ptr(), c.data_ptr(), s.data_ptr(), pages, bt.data_ptr(), table.shape[1],
+                                         1, r.data_ptr(), p.data_ptr(), n, w, raw.data_ptr() + 8, None, dsa._stream())
+    assert st == dsa.OK
+    dsa.check_device()
+    assert torch.equal(raw[4:].view(n, 64, 192), want) and not raw[:4].any()
 
 
 @pytest.mark.parametrize("w", [1, 9, 64, 100, 512])
@@ -170,8 +188,8 @@ def test_window_chunks_of_several_requests(w):
     pages = 30
     table = Q.random_table([900, 400], pages, w)
     cache, scale = Q.filled_cache(pages, w + 1)
-    pos = list(range(20)) + list(range(700, 741)) + list(range(260, 300)) + [5, 890, 5, 890, 300, 299, 298, 297, 64, 64, -1, 64, -1, -1, 399]
-    req = [0] * 61 + [1] * 40 + [0, 0, 1, 0, 1, 1, 1, 1, 0, 0, 0, 0, 1, 1, 1]
+    pos = list(range(100)) + list(range(700, 741)) + list(range(260, 300)) + [5, 890, 5, 890, 300, 299, 298, 297, 64, 64, -1, 64, -1, -1, 399]
+    req = [0] * 141 + [1] * 40 + [0, 0, 1, 0, 1, 1, 1, 1, 0, 0, 0, 0, 1, 1, 1]
     q = Q.rows((len(pos), 64, 192), w + 2, 0.3)
     out, lse = window(cache, scale, table, q, req, pos, w)
     ref = reference(cache, scale, table, q, req, pos, Q.window_tokens(pos, w))
@@ -181,30 +199,41 @@ def test_window_chunks_of_several_requests(w):
             assert not out[i].any() and torch.isinf(lse[i]).all()
 
 
+def test_rows_without_tokens_between_others():
+    # more rows than CTAs at once (each runs through several), one and two and none of them with tokens
+    pages, n, w = 4, 185, 1
+    table = Q.random_table([200], pages, 139)
+    cache, scale = Q.filled_cache(pages, 140)
+    pos = [-1 if i % 5 in (1, 2, 4) or 60 < i < 140 else i for i in range(n)]
+    q = Q.rows((n, 64, 192), 141, 0.3)
+    for _ in range(5):
+        out, lse = window(cache, scale, table, q, [0] * n, pos, w)
+        Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * n, pos, Q.window_tokens(pos, w)))
+    sel, cnt = Q.random_selection([max(p, 0) for p in pos], 3, 142)
+    out, lse = sparse(cache, scale, table, q, [0] * n, pos, sel, cnt)
+    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * n, pos, Q.sel_tokens(sel, cnt, pos)))
+
+
 def test_nan_at_a_token_that_some_of_a_chunk_attend():
     # V of two tokens: the newest one (the last query alone attends it) and the oldest of the first
     # query's window; the rest of the 8 stay finite
     pages = 14
     table = Q.random_table([800], pages, 130)
     cache, scale = Q.filled_cache(pages, 131)
-    pos = list(range(704, 744))
-    q = Q.rows((40, 64, 192), 132, 0.3)
-    clean, _ = window(cache, scale, table, q, [0] * 40, pos, 512)
-    for t, dim in ((743, 3), (704 - 511, 5)):
+    n = 200
+    pos = list(range(544, 744))
+    q = Q.rows((n, 64, 192), 132, 0.3)
+    for t, dim in ((743, 3), (544 - 511, 5)):
         cache[table[0, t // 64], :, t % 64 // 8, 1, t % 8, dim] = 0x7F
-    out, lse = window(cache, scale, table, q, [0] * 40, pos, 512)
+    out, lse = window(cache, scale, table, q, [0] * n, pos, 512)
     nan = torch.isnan(out)
-    assert nan[39, :, 3].all() and nan[0, :, 5].all() and int(nan.sum()) == 2 * 64
-    out[39, :, 3] = clean[39, :, 3]
-    out[0, :, 5] = clean[0, :, 5]
-    # the others: the two tokens' own other dims are as they were, so nothing else has changed but the
-    # order in which references move; both are within the tolerance of the same 64-bit rows
-    cache = cache.clone()
-    for t, dim in ((743, 3), (704 - 511, 5)):
+    assert nan[n - 1, :, 3].all() and nan[0, :, 5].all() and int(nan.sum()) == 2 * 64
+    # all else is what it is with a zero in their place
+    for t, dim in ((743, 3), (544 - 511, 5)):
         cache[table[0, t // 64], :, t % 64 // 8, 1, t % 8, dim] = 0
-    ref = list(reference(cache, scale, table, q, [0] * 40, pos, Q.window_tokens(pos, 512)))
-    for i, dim in ((39, 3), (0, 5)):
-        ref[0][i, :, dim] = out[i, :, dim].double().cpu().numpy()
+    ref = reference(cache, scale, table, q, [0] * n, pos, Q.window_tokens(pos, 512))
+    for i, dim in ((n - 1, 3), (0, 5)):
+        out[i, :, dim] = torch.from_numpy(ref[0][i, :, dim]).to(out)
     Q.check_attention(out, lse, ref)
 
 
@@ -212,9 +241,9 @@ def test_bad_pages_and_requests_in_a_chunk():
     pages = 10
     table = Q.random_table([500], pages, 133)
     cache, scale = Q.filled_cache(pages, 134)
-    pos = list(range(450, 490))
-    req = [0] * 40
-    q = Q.rows((40, 64, 192), 135, 0.3)
+    pos = list(range(290, 490))
+    req = [0] * 200
+    q = Q.rows((200, 64, 192), 135, 0.3)
     bad = table.copy()
     bad[0, 5] = pages                                              # tokens 320 .. 383
     out, lse = window(cache, scale, bad, q, req, pos, 200, check=False)
@@ -227,12 +256,12 @@ def test_bad_pages_and_requests_in_a_chunk():
     out, lse = window(cache, scale, table, q, req, pos, 200, check=False)
     with pytest.raises(dsa.DsaError):
         dsa.check_device()
-    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 40, pos,
+    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 200, pos,
                                           lambda i, g: tok(i, g)[:0] if i == 11 else tok(i, g)))
-    out, lse = window(cache, scale, table[:, :7], q, [0] * 40, pos, 200, check=False)       # the table ends at token 447
+    out, lse = window(cache, scale, table[:, :7], q, [0] * 200, pos, 200, check=False)       # the table ends at token 447
     with pytest.raises(dsa.DsaError):
         dsa.check_device()
-    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 40, pos, lambda i, g: tok(i, g)[tok(i, g) < 448]))
+    Q.check_attention(out, lse, reference(cache, scale, table, q, [0] * 200, pos, lambda i, g: tok(i, g)[tok(i, g) < 448]))
 
 
 def test_window_over_a_ring():
