@@ -9,13 +9,13 @@ namespace dsa {
 namespace attnqt {
 
 using attnq::ex2;
-using attnq::kInRow;
 using attnq::kRegBytes;
 using attnq::Params;
 
 constexpr int kTileRegions = 16;                                 // 128 tokens: the MMA's M
 constexpr int kTileBytes = kTileRegions * kRegBytes;             // 48 KiB
 constexpr int kStages = 2;
+constexpr int kInRow = kD + 4;                                   // inbox row: O, m, M, l, pad
 constexpr int kThreads = 192;                                    // warps 0-3 softmax, 4 loads, 5 MMA
 constexpr int kCtasPerSm = 2;
 constexpr int kN = 32;                                           // S: 16 heads x (hi, lo) of q
@@ -296,18 +296,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             int i_s = 0, i_p = 0, i = 0, j = 0;
             int n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
             int reg_p = r_p < rows ? row_of(p, r_p, rank, false).n_reg : 0;
-            bool ok = true, have_q = false;
+            bool ok = true;
             long long since = clock64();
             while (ok) {
-                // the q of every row is waited for in turn, that of a row without tiles too (a barrier's
-                // parity tells a phase from the next, not from the one after that)
-                if (!have_q && r_s < rows) have_q = mbar_test(&sm.q_ready, rows_s & 1u);
-                if (have_q && i_s == n_s) {
+                // (q_ready's phases count the rows with tiles: after one of them the softmax waits for its
+                // S before it puts the next q, so a parity is never one phase off)
+                while (r_s < rows && i_s == n_s) {
                     r_s += step;
-                    ++rows_s;
+                    if (n_s > 0) ++rows_s;
                     i_s = 0;
                     n_s = r_s < rows ? row_of(p, r_s, rank, false).n_tiles : 0;
-                    have_q = false;
                 }
                 while (r_p < rows && i_p * kTileRegions >= reg_p) {
                     r_p += step;
@@ -334,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     ++j;
                     ++i_p;
                     since = clock64();
-                } else if (have_q && i_s < n_s && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u)) {
+                } else if (r_s < rows && i < j + 2 && mbar_test(&sm.full[i % kStages], (unsigned)(i / kStages) & 1u) &&
+                           (i_s > 0 || mbar_test(&sm.q_ready, rows_s & 1u))) {
                     tc_fence_after();
                     const uint32_t a = k_lo + (uint32_t)(i % kStages) * (kTileBytes >> 4), d = tmem + 32 * (i & 1);
                     mma_f8<false>(d, a, kKvHi, q_lo, kQHi, kIdescS);
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int j = 0; j < 3; ++j) qv[j] = __ldg(src + 8 * j);
         };
-        auto put_q = [&]() {
+        auto put_q = [&](bool tiles) {                           // (no S waits for the q of a row without tiles)
             const int h = tid >> 3, c = tid & 7;
             __nv_bfloat162 a2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
@@ -408,14 +407,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_ready);
+            if (lane == 0 && tiles) mbar_arrive(&sm.q_ready);
         };
         int tg = 0;                                              // tiles before this one, over all rows
         Row x{}, x_next{};
         if (first < rows) {
             load_q(first);
             x_next = row_of(p, first, rank, false);
-            put_q();
+            put_q(x_next.n_tiles > 0);
         }
         for (unsigned rr = first; rr < rows; rr += step) {
             x = x_next;
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (tid == 0) mbar_arrive(&sm.p_ready);
             }
             // every S of this row is done with its q: the next row's
-            if (rr + step < rows) put_q();
+            if (rr + step < rows) put_q(x_next.n_tiles > 0);
             // ---- the CTA's sums and factors
             {
                 float v[16];

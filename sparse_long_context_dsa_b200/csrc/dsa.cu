@@ -1272,17 +1272,22 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
         return launch_k("window_attn_band_kernel", dsa::attnqb::window_attn_band_kernel, dim3((unsigned)blocks),
                         dim3(dsa::attnqb::kThreads), dsa::attnqb::kSmemBytes, stream, 0, map, p);
     }
-    // CTAs per row: as many as fit the GPU at once, while each keeps half a tile of regions
+    // CTAs per row: as many as the GPU holds at once, while each keeps half a tile of regions.  A
+    // cluster lies within one of the chip's groups of SMs, and what is left over in each (even, up to
+    // S - 2 CTAs) stays empty: a row more than fit costs a second round.  k = 512 at 32,768 tokens, us
+    // with S against S / 2 CTAs: S = 16 at 8 rows 11.7 / 14.0, 12 rows 12.1 / 15.3, 16 rows 22.4 / 15.8;
+    // S = 8 at 32 rows 19.2 / 25.3, 36 rows 32.1 / 26.5; S = 4 at 68 rows 30.1 / 42.7, 72 rows 48.5 /
+    // 42.3; S = 2 at 148 rows 49.5 / 64.2.
     const int64_t rows = (int64_t)nq * dsa::kG;
     const int most = window > 0 ? window_regions(window) : k;
     p.splits = 1;
-    while (p.splits < 16 && rows * p.splits * 2 <= resident && most >= 2 * p.splits * (dsa::attnqt::kTileRegions / 2))
-        p.splits *= 2;
+    for (int s = 2; s <= 16 && rows * s <= resident - 6 * (s - 2) && most >= s * (dsa::attnqt::kTileRegions / 2); s *= 2)
+        p.splits = s;
     p.per = (most + p.splits - 1) / p.splits;
     // one CTA after another takes the rows where there are more than CTAs at once
     const int64_t ctas = p.splits > 1 ? rows * p.splits : std::min<int64_t>(rows, resident);
-    return launch_k("sparse_attn_quant_tc_kernel", dsa::attnqt::sparse_attn_quant_tc_kernel, dim3((unsigned)ctas), dim3(dsa::attnqt::kThreads), dsa::attnqt::kSmemBytes, stream,
-                    p.splits > 1 ? (unsigned)p.splits : 0u, map, p);
+    return launch_k("sparse_attn_quant_tc_kernel", dsa::attnqt::sparse_attn_quant_tc_kernel, dim3((unsigned)ctas),
+                    dim3(dsa::attnqt::kThreads), dsa::attnqt::kSmemBytes, stream, p.splits > 1 ? (unsigned)p.splits : 0u, map, p);
 }
 }  // namespace
 
