@@ -209,7 +209,7 @@ struct Pools {
             const at::Tensor &t = THPVariable_Unpack(o);
             if (!t.is_cuda() || !t.is_contiguous() || t.dim() < 2 || t.size(0) != n_pages) throw Refused();
             pool[i].data = t.data_ptr();
-            pool[i].page_bytes = t.stride(0) * (int64_t)t.element_size();
+            pool[i].page_bytes = n_pages > 0 ? t.numel() / n_pages * (int64_t)t.element_size() : 0;
         }
     }
 };

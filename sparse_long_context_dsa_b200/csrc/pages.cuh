@@ -15,6 +15,8 @@
 // Bound: HBM, every moved page read and written once; the counts and tables are small beside it.
 #pragma once
 
+#include <climits>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -222,12 +224,26 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(int32_t *ref_out, int64_
     const int L = length[i], full = L / kPage;
     const int32_t *from = table_in + (int64_t)parent[i] * max_pages;
     int32_t *to = table_out + (int64_t)c * max_pages;
+    // whether somebody held the page before the call: a count above 0 that no fork of this call set
+    // (`fresh` ascends; most pages lie outside its range)
+    const int n_fresh = (int)min((int64_t)n, n_pages - *n_live);
+    const int fresh_lo = n_fresh > 0 ? fresh[0] : INT_MAX, fresh_hi = n_fresh > 0 ? fresh[n_fresh - 1] : -1;
+    auto held = [&](int page) {
+        if (page < 0 || page >= n_pages || ref_out[page] <= 0) return false;
+        if (page < fresh_lo || page > fresh_hi) return true;
+        int a = 0, b = n_fresh;
+        while (a < b) {
+            const int mid = (a + b) / 2;
+            if (fresh[mid] < page) a = mid + 1;
+            else b = mid;
+        }
+        return fresh[a] != page;                           // (a < n_fresh: page <= fresh_hi)
+    };
     int src = -1, dst = -1;
     if (L % kPage) {
         src = from[full];
-        if (src < 0 || src >= n_pages) src = -1;
-        if (src >= 0 && rank < n_pages - *n_live) dst = fresh[rank];
-        if (dst < 0 && lead) set_error(kErrPages);         // a bad page, or none free
+        if (rank < n_fresh && held(src)) dst = fresh[rank];
+        if (dst < 0 && lead) set_error(kErrPages);         // a page that nobody holds, or none free
     }
     if (dst >= 0)
         for (int seg = blockIdx.x; seg < pools.first[pools.n]; seg += gridDim.x) copy_segment(pools, seg, src, dst);
@@ -235,8 +251,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(int32_t *ref_out, int64_
         int page = -1;
         if (v < full) {
             page = from[v];
-            // a page that nobody holds cannot be shared
-            if (page < 0 || page >= n_pages || ref_out[page] <= 0) {
+            if (!held(page)) {                             // it cannot be shared
                 set_error(kErrPages);
                 page = -1;
             } else {

@@ -35,7 +35,7 @@ def fork(ref, table, parent, child, length, pools):
                 errors += 1
         if L % PAGE:
             p = src_table[b, full]
-            if 0 <= p < len(ref) and j < len(free):
+            if 0 <= p < len(ref) and ref0[p] > 0 and j < len(free):
                 row[full] = free[j]
                 ref[free[j]] = 1
                 for x in pools:
@@ -164,6 +164,15 @@ def test_bad_forks_are_flagged_and_do_nothing(parent, child, length):
 def test_forks_without_a_free_page():
     ref, table, pools = pool_of([300, 200], 11, 4, rows=6)          # 9 pages held, 2 free
     run_fork(ref, table, [0, 1, 0, 1], [2, 3, 4, 5], [299, 199, 128, 190], pools, True)
+
+
+def test_parents_entries_that_name_free_pages():
+    # among them the pages that this call's forks copy into
+    ref, table, pools = pool_of([300, 200, 700], 60, 14, rows=12)
+    free = np.nonzero(ref <= 0)[0]
+    table[0, 0], table[0, 4], table[1, 1], table[1, 3], table[2, 2] = free[0], free[1], free[2], free[0], free[9]
+    for _ in range(5):
+        run_fork(ref, table, [0, 1, 2, 0, 1, 2, 2], [4, 5, 6, 7, 8, 9, 10], [299, 198, 650, 256, 130, 699, 450], pools, True)
 
 
 @pytest.mark.parametrize("in_place", [True, False])
