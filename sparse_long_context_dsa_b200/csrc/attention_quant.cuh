@@ -30,6 +30,7 @@ struct Params {
     float scale_log2;            // log2(e) / sqrt(192)
     int splits;                  // row kernel: CTAs (the cluster) per row: 1, 2, 4, 8 or 16
     int per;                     // regions of a row for each of them
+    unsigned row0, row_end;      // row kernel: the launch's rows, of nq * 4
 };
 
 // A pair of e4m3 codes -> fp16 (exact).

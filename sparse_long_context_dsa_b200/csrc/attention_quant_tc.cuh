@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     // This CTA's rows: with S = 1 every gridDim.x-th one (the ring, the barriers' phases and the
     // tiles' count `base` run through them all), else the cluster's one.
-    const unsigned rows = (unsigned)p.nq * kG;
-    const unsigned first = blockIdx.x / (unsigned)S, step = gridDim.x / (unsigned)S;
+    const unsigned rows = p.row_end;
+    const unsigned first = p.row0 + blockIdx.x / (unsigned)S, step = gridDim.x / (unsigned)S;
     const int rank = (int)(blockIdx.x % (unsigned)S);
 
     if (warp == 4) {

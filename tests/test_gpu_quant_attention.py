@@ -72,6 +72,21 @@ def test_prefill_queries_of_several_requests():
     sparse_case(lengths, 60, 80, pos, req, prefill=True)
 
 
+@pytest.mark.parametrize("n,k", [(75, 128), (90, 200), (110, 192)])
+def test_rows_behind_the_last_full_round(n, k):
+    # more rows than CTAs at once, the rest of them few enough to be split in a launch of its own
+    lengths = [1700, 2100]
+    pages = 80
+    table = Q.random_table(lengths, pages, 151)
+    cache, scale = Q.filled_cache(pages, 152)
+    req = [i % 2 for i in range(n)]
+    pos = [lengths[r] - 1 - 3 * i for i, r in enumerate(req)]
+    q = Q.rows((n, 64, 192), 153, 0.3)
+    sel, cnt = Q.random_selection(pos, k, 154)
+    out, lse = sparse(cache, scale, table, q, req, pos, sel, cnt)
+    Q.check_attention(out, lse, reference(cache, scale, table, q, req, pos, Q.sel_tokens(sel, cnt, pos)))
+
+
 def test_every_offset_of_the_own_region():
     pos = list(range(160, 176))
     sparse_case([176], 1, 81, pos, [0] * 16, prefill=True)
