@@ -35,9 +35,9 @@ using attnqt::mma_f8;
 constexpr int kQueries = 8;
 constexpr int kTileBytes = quant::kRegionsPerPage * kRegBytes;   // a page of one group: 24 KiB
 constexpr int kStages = 4;
-constexpr int kThreads = 192;                                    // warps 0-3 softmax, 4 MMA, 5 loads
+constexpr int kThreads = 320;                                    // warps 0-3, 4-7 softmax of even and odd tiles, 8 MMA, 9 loads
 constexpr int kSpan = 56;                                        // positions of a run lie this close to its first
-constexpr int kOCol = 128;                                       // TMEM: S 0, 64; O 128 .. 319
+constexpr int kOCol = 128;                                       // TMEM: S 0, 64; O 128 .. 319, 320 .. 511 (even and odd tiles)
 constexpr int kTmemCols = 512;
 constexpr float kBase = 5.0f;                                    // log2 of a weight at its reference
 constexpr float kSlack = 10.0f;                                  // log2 units a reference may lag behind
@@ -48,10 +48,11 @@ struct Smem {
     float4 scale[kStages][8];                                    // K's, V's, log2 of V's
     int there[kStages];                                          // the page is there
     float qscale[128];
+    float4 merge[2][128];                                        // m, M, l of a row's even and odd tiles
     int pos[kQueries], req[kQueries];
     int run_end[kQueries];                                       // first query behind the run that begins here
     int nan[2];                                                  // run n (by parity) met a NaN code at a partly attended token: n + 1
-    uint64_t full[kStages], empty[kStages], s_full[2], p_ready[2], pv_done[2], run_done, drain;
+    uint64_t full[kStages], empty[kStages], s_full[2], s_read[2], p_ready[2], pv_done[2], merged, run_done, drain;
     uint32_t tmem;
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
@@ -110,15 +111,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_read[i], 4);
             mbar_init(&sm.p_ready[i], 4);
             mbar_init(&sm.pv_done[i], 1);
         }
-        mbar_init(&sm.run_done, 6);                              // every role: none is two runs behind another
+        mbar_init(&sm.merged, 8);
+        mbar_init(&sm.run_done, 10);                             // every role: none is two runs behind another
         mbar_init(&sm.drain, 1);
         sm.nan[0] = sm.nan[1] = 0;
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc(&sm.tmem, kTmemCols);
+    if (warp == 8) tmem_alloc(&sm.tmem, kTmemCols);
     pdl_wait();      // the previous kernel's results are visible from here on
     const int blocks = (p.nq + kQueries - 1) / kQueries;
     const int g = (int)blockIdx.x / blocks, q0 = ((int)blockIdx.x % blocks) * kQueries;
@@ -148,24 +151,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem;
     // q of every query: 2^-e q = hi + lo in e4m3; 8 threads share a head, thread c of them holds dims
     // 8 c .. 8 c + 7 of every 64-dim block
-    if (warp < 4) {
-        const int h = tid >> 3, c = tid & 7;
+    if (warp < 8) {
+        const int h = (tid >> 3) & 15, c = tid & 7, even = tid >> 7;     // queries even, even + 2, ..
         const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((int64_t)q0 * kHQ + g * kHeadsPerGroup + h) * kD + 8 * c);
         constexpr int kNext = kHQ * kD / 8;                      // 16-byte pieces from one query to the next
         uint4 ahead[2][3];                                       // the next two queries' pieces, in flight
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 3; ++j) ahead[u][j] = u < n_q ? __ldg(src + u * kNext + 8 * j) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < 3; ++j)
+                ahead[u][j] = even + 2 * u < n_q ? __ldg(src + (even + 2 * u) * kNext + 8 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-        for (int u = 0; u < n_q; ++u) {
+        for (int u = even; u < n_q; u += 2) {
             uint4 qv[3];
             __nv_bfloat162 a2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
                 qv[j] = ahead[0][j];
                 ahead[0][j] = ahead[1][j];
-                if (u + 2 < n_q) ahead[1][j] = __ldg(src + (u + 2) * kNext + 8 * j);
+                if (u + 4 < n_q) ahead[1][j] = __ldg(src + (u + 4) * kNext + 8 * j);
                 const uint32_t w[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a2 = __hmax2(a2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int tg = 0;                                                  // tiles before this one, over all runs
 
-    if (warp == 5) {
+    if (warp == 9) {
         // ---- loads: a page of the group at a time
         while (u0 < n_q && ok) {
             const Run r = run_at(sm, p, u0, u0 < single_until);
@@ -255,51 +259,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&sm.full[s], (unsigned)(last / kStages) & 1u);
             }
         __syncwarp();
-    } else if (warp == 4) {
-        // ---- MMA issuer (one lane): S(i), then O += P'(i - 1) V(i - 1)
+    } else if (warp == 8) {
+        // ---- MMA issuer (one lane): S of two tiles ahead, then O += P'(j) V(j) as the weights are there
         if (lane == 0) {
             // K rows of 64 bytes, 8 of a region 512 bytes, regions 3 KiB apart; V^T: 64-dim blocks 1 KiB
             // apart, 8-token groups 3 KiB apart; q and P': rows of 64 bytes
             const uint32_t k_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring) + 512, 1024);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
-            int j = 0;                                           // P' V issued, over all runs
-            auto issue_pv = [&](bool fresh) {
+            auto issue_s = [&](int i) {
+                const int st = i % kStages;
+                ok = ok && mbar_wait(&sm.full[st], (unsigned)(i / kStages) & 1u);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t b = k_lo + (uint32_t)st * (kTileBytes >> 4), d = tmem + 64 * (i & 1);
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int ks = 0; ks < 6; ++ks) {
+                        const uint32_t a = desc_lo(smem_u32(sm.q[term]) + (ks >> 1) * 8192 + (ks & 1) * 32, 16);
+                        const uint32_t bk = b + (((ks >> 1) * 1024 + (ks & 1) * 32) >> 4);
+                        if (term == 0 && ks == 0) mma_f8<false>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                        else mma_f8<true>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                    }
+                umma_commit(&sm.s_full[i & 1]);
+            };
+            auto issue_pv = [&](int j, bool fresh) {
                 ok = ok && mbar_wait(&sm.p_ready[j & 1], (unsigned)(j >> 1) & 1u);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t b = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4);
+                const uint32_t b = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4), d = tmem + kOCol + kD * (j & 1);
 #pragma unroll
                 for (int term = 0; term < 3; ++term) {
                     const uint32_t a = desc_lo(smem_u32(sm.p[j & 1][term]), 16);
-                    if (term == 0 && fresh) mma_f8<false>(tmem + kOCol, a, kRowsHi, b, kKvHi, kIdescO);
-                    else mma_f8<true>(tmem + kOCol, a, kRowsHi, b, kKvHi, kIdescO);
-                    mma_f8<true>(tmem + kOCol, a + (32 >> 4), kRowsHi, b + (4 * kRegBytes >> 4), kKvHi, kIdescO);
+                    if (term == 0 && fresh) mma_f8<false>(d, a, kRowsHi, b, kKvHi, kIdescO);
+                    else mma_f8<true>(d, a, kRowsHi, b, kKvHi, kIdescO);
+                    mma_f8<true>(d, a + (32 >> 4), kRowsHi, b + (4 * kRegBytes >> 4), kKvHi, kIdescO);
                 }
                 umma_commit(&sm.empty[j % kStages]);
                 umma_commit(&sm.pv_done[j & 1]);
-                ++j;
             };
             while (u0 < n_q && ok) {
                 const Run r = run_at(sm, p, u0, u0 < single_until);
+                for (int ti = 0; ti < min(2, r.tiles); ++ti) issue_s(tg + ti);
                 for (int ti = 0; ti < r.tiles && ok; ++ti, ++tg) {
-                    const int st = tg % kStages;
-                    ok = mbar_wait(&sm.full[st], (unsigned)(tg / kStages) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t b = k_lo + (uint32_t)st * (kTileBytes >> 4), d = tmem + 64 * (tg & 1);
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int ks = 0; ks < 6; ++ks) {
-                            const uint32_t a = desc_lo(smem_u32(sm.q[term]) + (ks >> 1) * 8192 + (ks & 1) * 32, 16);
-                            const uint32_t bk = b + (((ks >> 1) * 1024 + (ks & 1) * 32) >> 4);
-                            if (term == 0 && ks == 0) mma_f8<false>(d, a, kRowsHi, bk, kKvHi, kIdescS);
-                            else mma_f8<true>(d, a, kRowsHi, bk, kKvHi, kIdescS);
-                        }
-                    umma_commit(&sm.s_full[tg & 1]);
-                    if (ti > 0) issue_pv(ti == 1);
+                    if (ti + 2 < r.tiles) {
+                        ok = ok && mbar_wait(&sm.s_read[tg & 1], (unsigned)(tg >> 1) & 1u);
+                        if (ok) issue_s(tg + 2);
+                    }
+                    issue_pv(tg, ti < 2);
                 }
-                if (r.tiles > 0) issue_pv(r.tiles == 1);
                 if (ok) mbar_arrive(&sm.run_done);
                 ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
                 next(r);
@@ -310,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread = row 16 u + h
-        const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
-        const int u = tid >> 4;
-        const float qf = sm.qscale[tid];
-        const int64_t head = (int64_t)(q0 + u) * kHQ + g * kHeadsPerGroup + (tid & 15);
+        // ---- softmax: thread = row 16 u + h, the tiles of its group's parity
+        const int grp = tid >> 7, row = tid & 127, wg = warp & 3, u = row >> 4;
+        const uint32_t trow = tmem + ((uint32_t)(32 * wg) << 16), tcol_o = trow + kOCol + kD * grp;
+        const float qf = sm.qscale[row];
+        const int64_t head = (int64_t)(q0 + u) * kHQ + g * kHeadsPerGroup + (row & 15);
         bool landed = true;
         // a wait that gives up leaves the error flag and garbage; the later ones are then short
         auto wait = [&](uint64_t *bar, unsigned parity) {
@@ -332,16 +340,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m = -INFINITY, M = -INFINITY, mref = 0.0f, c = 0.0f, l = 0.0f;
             for (int ti = 0; ti < r.tiles; ++ti, ++tg) {
+                if ((tg & 1) != grp) continue;
                 const int st = tg % kStages, t0 = (r.lo / kPage + ti) * kPage;
                 wait(&sm.full[st], (unsigned)(tg / kStages) & 1u);
                 const bool there = sm.there[st] != 0;
                 const bool whole = there && t0 >= all_lo && t0 + kPage - 1 <= all_hi;
-                if (!whole && tid < kPage) {
+                if (!whole && row < kPage) {
                     // V rows that nobody attends: zero; that some attend: looked at for NaN
-                    const int t = t0 + tid;
+                    const int t = t0 + row;
                     const bool none = !there || t < r.lo || t > r.hi;
                     if (none || t < all_lo || t > all_hi) {
-                        uint8_t *v = ring + st * kTileBytes + (tid >> 3) * kRegBytes + 512 + (tid & 7) * 64;
+                        uint8_t *v = ring + st * kTileBytes + (row >> 3) * kRegBytes + 512 + (row & 7) * 64;
                         bool bad = false;
 #pragma unroll 4
                         for (int i = 0; i < 12; ++i) {
@@ -357,13 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (bad) sm.nan[n_run & 1] = n_run + 1;
                     }
                 }
-                wait(&sm.s_full[tg & 1], (unsigned)(tg >> 1) & 1u);
+                wait(&sm.s_full[grp], (unsigned)(tg >> 1) & 1u);
                 __syncwarp();
                 tc_fence_after();
                 float s[64];
                 {
                     float a[32], b[32];
-                    tmem_ld32x2(trow + 64 * (tg & 1), trow + 64 * (tg & 1) + 32, a, b);
+                    tmem_ld32x2(trow + 64 * grp, trow + 64 * grp + 32, a, b);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         s[i] = a[i];
@@ -371,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_read[grp]);
                 float mx = -INFINITY, mv = -INFINITY;
                 if (whole && __all_sync(0xffffffffu, mine)) {
 #pragma unroll
@@ -402,6 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mv = fmaxf(mv, y + sc.z);
                     }
                 }
+                // this group's tile before (tg - 2) is in O, and its P' has been read
+                if (ti >= 2) wait(&sm.pv_done[grp], (unsigned)((tg - 2) >> 1) & 1u);
+                __syncwarp();
                 // the references move where a token passes one by more than the slack, or there is none
                 const bool grow = mx > m + kSlack || mv > M + kSlack || (M == -INFINITY && mx > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
@@ -416,22 +430,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         c = d == -INFINITY ? 0.0f : exp2f(fminf(a - d, 126.0f));
                         l *= al;
                     }
-                    if (ti > 0 && __any_sync(0xffffffffu, ao != 1.0f)) {
-                        // O holds the tiles before this one once their MMAs are done
-                        wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
-                        __syncwarp();
+                    if (ti >= 2 && __any_sync(0xffffffffu, ao != 1.0f)) {
                         tc_fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < kD; c0 += 64) {
                             float o[32], o2[32];
-                            tmem_ld32x2(trow + kOCol + c0, trow + kOCol + c0 + 32, o, o2);
+                            tmem_ld32x2(tcol_o + c0, tcol_o + c0 + 32, o, o2);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 o[i] *= ao;
                                 o2[i] *= ao;
                             }
-                            tmem_st32(trow + kOCol + c0, o);
-                            tmem_st32(trow + kOCol + c0 + 32, o2);
+                            tmem_st32(tcol_o + c0, o);
+                            tmem_st32(tcol_o + c0 + 32, o2);
                         }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tc_fence_before();
@@ -439,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // P' in three e5m2 terms: the upper bytes of w, of what they leave, and of the rest,
                 // rounded; 16 tokens at a time
-                uint8_t *dst = sm.p[tg & 1][0] + tid * 64;
+                uint8_t *dst = sm.p[grp][0] + row * 64;
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     uint32_t w[8];
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[4 * hf + i] = attnq::pack_f16x2(p0 * f, p1 * f);
                         }
                     }
-                    const int at = (ch ^ ((tid >> 1) & 3)) << 4;
+                    const int at = (ch ^ ((row >> 1) & 3)) << 4;
 #pragma unroll
                     for (int term = 0; term < 3; ++term) {
                         if (term == 2) {
@@ -472,38 +483,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_ready[tg & 1]);
+                if (lane == 0) mbar_arrive(&sm.p_ready[grp]);
             }
-            // ---- the run's rows
-            if (r.tiles > 0) wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
+            // ---- the run's rows: the two groups' sums and references meet, each group writes half of the dims
+            sm.merge[grp][row] = make_float4(m, M, l, 0.0f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.merged);
+            for (int x = max(tg - 2, tg - r.tiles); x < tg; ++x) wait(&sm.pv_done[x & 1], (unsigned)(x >> 1) & 1u);
+            wait(&sm.merged, (unsigned)n_run & 1u);
             __syncwarp();
             tc_fence_after();
-            // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
-            const float f = l > 0.0f ? (M > -INFINITY ? exp2f(M - m) / l : 0.0f) : l;
-            // through shared memory (this warp's share of the P' tiles, which its last MMAs have read), so
-            // that a warp writes whole rows of the output: 32 rows of 384 B, 16-byte pieces XORed by the row
-            uint8_t *rows = sm.p[0][0] + warp * (32 * 2 * kD);
+            float w[2] = {0.0f, 0.0f};                           // of each group's O
+            {
+                const float4 a = sm.merge[0][row], b = sm.merge[1][row];
+                m = fmaxf(a.x, b.x);
+                M = fmaxf(a.y, b.y);
+                // (a sum without a reference is 0 or NaN)
+                l = (a.x == -INFINITY ? a.z : a.z * exp2f(a.x - m)) + (b.x == -INFINITY ? b.z : b.z * exp2f(b.x - m));
+                // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
+                const float f = l > 0.0f ? (M > -INFINITY ? exp2f(M - m) / l : 0.0f) : l;
+                w[0] = a.y == -INFINITY ? 0.0f : exp2f(a.y - M);
+                w[1] = b.y == -INFINITY ? 0.0f : exp2f(b.y - M);
+                w[0] *= f;
+                w[1] *= f;
+            }
+            const bool has[2] = {r.tiles >= 2 || (r.tiles == 1 && ((tg - 1) & 1) == 0), r.tiles >= 2 || (r.tiles == 1 && ((tg - 1) & 1) == 1)};
+            // through shared memory (this warp's share of the P' tiles, which the last MMAs have read), so that
+            // a warp writes whole lines of the output: 32 rows of 192 B, 16-byte pieces XORed by the row
+            uint8_t *rows = sm.p[0][0] + warp * (32 * kD);
 #pragma unroll 1
-            for (int c0 = 0; c0 < kD; c0 += 32) {
+            for (int c0 = 0; c0 < kD / 2; c0 += 32) {
                 float o[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-                if (r.tiles > 0) tmem_ld32(trow + kOCol + c0, o);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (has[b]) {
+                        float x[32];
+                        tmem_ld32(trow + kOCol + kD * b + (kD / 2) * grp + c0, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = fmaf(x[i], w[b], o[i]);
+                    }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(rows + lane * (2 * kD) + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                                   pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+                    *reinterpret_cast<uint4 *>(rows + lane * kD + (((c0 / 8 + i) ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                   pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
             }
             __syncwarp();
             // (out is 8-byte aligned: two stores of 8 bytes where it is not 16-byte aligned)
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-            int row = lane / 24, piece = lane % 24;              // 24 pieces of 16 bytes a row, 32 at a time
-#pragma unroll 8
-            for (int i = 0; i < 24; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(rows + row * (2 * kD) + ((piece ^ (row & 7)) << 4));
-                const int v = 2 * warp + (row >> 4);
-                __nv_bfloat16 *dst = p.out + ((int64_t)(q0 + v) * kHQ + g * kHeadsPerGroup + (row & 15)) * kD + 8 * piece;
+#pragma unroll
+            for (int i = 0; i < 12; ++i) {                       // 12 pieces of 16 bytes a row, 32 at a time
+                const int e = lane + 32 * i, rw = e / 12, piece = e % 12;
+                const uint4 x = *reinterpret_cast<const uint4 *>(rows + rw * kD + ((piece ^ ((rw >> 1) & 3)) << 4));
+                const int v = 2 * wg + (rw >> 4);
+                __nv_bfloat16 *dst = p.out + ((int64_t)(q0 + v) * kHQ + g * kHeadsPerGroup + (rw & 15)) * kD + (kD / 2) * grp + 8 * piece;
                 if (v >= r.u0 && v < r.u1) {
                     if (wide) {
                         *reinterpret_cast<uint4 *>(dst) = x;
@@ -512,12 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         reinterpret_cast<uint2 *>(dst)[1] = make_uint2(x.z, x.w);
                     }
                 }
-                piece += 8;
-                row += piece >= 24 ? 2 : 1;
-                piece -= piece >= 24 ? 24 : 0;
             }
             __syncwarp();
-            if (mine && p.lse) p.lse[head] = l == 0.0f ? -INFINITY : (m - kBase + log2f(l)) * 0.69314718055994531f;
+            if (mine && grp == 0 && p.lse) p.lse[head] = l == 0.0f ? -INFINITY : (m - kBase + log2f(l)) * 0.69314718055994531f;
             tc_fence_before();
             fence_proxy_async();
             // every warp has looked at the run's tokens (sm.nan) before any role goes on
@@ -531,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();                                             // every role is done (or gave up)
     tc_fence_after();
-    if (warp == 4) tmem_free(tmem, kTmemCols);
+    if (warp == 8) tmem_free(tmem, kTmemCols);
 }
 
 }  // namespace attnqb
