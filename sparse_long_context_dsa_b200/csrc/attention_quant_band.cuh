@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid < kQueries) {
-        const int p0 = sm.pos[tid];
-        int e = tid + 1;
-        while (p0 >= 0 && e < kQueries && sm.pos[e] >= 0 && sm.req[e] == sm.req[tid] && abs(sm.pos[e] - p0) <= kSpan) ++e;
-        sm.run_end[tid] = e;
+    if (warp == 9 && lane < kQueries) {
+        const int p0 = sm.pos[lane];
+        int e = lane + 1;
+        while (p0 >= 0 && e < kQueries && sm.pos[e] >= 0 && sm.req[e] == sm.req[lane] && abs(sm.pos[e] - p0) <= kSpan) ++e;
+        sm.run_end[lane] = e;
     }
     const uint32_t tmem = sm.tmem;
     // q of every query: 2^-e q = hi + lo in e4m3; 8 threads share a head, thread c of them holds dims
@@ -200,7 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async();
     }
-    __syncthreads();                                             // q, the runs
+    // q, the runs; the loads' warp does not wait for q
+    __syncwarp();
+    if (warp == 9) asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+    else asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 
     // Every role walks the same runs: after a run that met a NaN (read behind the run's barrier), its
     // queries one by one.
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             // (out is 8-byte aligned: two stores of 8 bytes where it is not 16-byte aligned)
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 12; ++i) {                       // 12 pieces of 16 bytes a row, 32 at a time
                 const int e = lane + 32 * i, rw = e / 12, piece = e % 12;
                 const uint4 x = *reinterpret_cast<const uint4 *>(rows + rw * kD + ((piece ^ ((rw >> 1) & 3)) << 4));
