@@ -35,7 +35,7 @@ using attnqt::mma_f8;
 constexpr int kQueries = 8;
 constexpr int kTileBytes = quant::kRegionsPerPage * kRegBytes;   // a page of one group: 24 KiB
 constexpr int kStages = 4;
-constexpr int kThreads = 320;                                    // warps 0-3, 4-7 softmax of even and odd tiles, 8 MMA, 9 loads
+constexpr int kThreads = 352;                                    // warps 0-3, 4-7 softmax of even and odd tiles, 8 S, 9 loads, 10 P' V
 constexpr int kSpan = 56;                                        // positions of a run lie this close to its first
 constexpr int kOCol = 128;                                       // TMEM: S 0, 64; O 128 .. 319, 320 .. 511 (even and odd tiles)
 constexpr int kTmemCols = 512;
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.pv_done[i], 1);
         }
         mbar_init(&sm.merged, 8);
-        mbar_init(&sm.run_done, 10);                             // every role: none is two runs behind another
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.run_done, 11);                             // every role: none is two runs behind another
+        mbar_init(&sm.drain, 2);
         sm.nan[0] = sm.nan[1] = 0;
         fence_mbar_init();
     }
@@ -263,59 +263,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         __syncwarp();
     } else if (warp == 8) {
-        // ---- MMA issuer (one lane): S of two tiles ahead, then O += P'(j) V(j) as the weights are there
+        // ---- S, at most two tiles ahead of the weights (one lane).  K: rows of 64 bytes, 8 of a region
+        // 512 bytes, regions 3 KiB apart; q: rows of 64 bytes
         if (lane == 0) {
-            // K rows of 64 bytes, 8 of a region 512 bytes, regions 3 KiB apart; V^T: 64-dim blocks 1 KiB
-            // apart, 8-token groups 3 KiB apart; q and P': rows of 64 bytes
-            const uint32_t k_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring) + 512, 1024);
+            const uint32_t k_lo = desc_lo(smem_u32(ring), 16);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
-            auto issue_s = [&](int i) {
-                const int st = i % kStages;
-                ok = ok && mbar_wait(&sm.full[st], (unsigned)(i / kStages) & 1u);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t b = k_lo + (uint32_t)st * (kTileBytes >> 4), d = tmem + 64 * (i & 1);
-#pragma unroll
-                for (int term = 0; term < 2; ++term)
-#pragma unroll
-                    for (int ks = 0; ks < 6; ++ks) {
-                        const uint32_t a = desc_lo(smem_u32(sm.q[term]) + (ks >> 1) * 8192 + (ks & 1) * 32, 16);
-                        const uint32_t bk = b + (((ks >> 1) * 1024 + (ks & 1) * 32) >> 4);
-                        if (term == 0 && ks == 0) mma_f8<false>(d, a, kRowsHi, bk, kKvHi, kIdescS);
-                        else mma_f8<true>(d, a, kRowsHi, bk, kKvHi, kIdescS);
-                    }
-                umma_commit(&sm.s_full[i & 1]);
-            };
-            auto issue_pv = [&](int j, bool fresh) {
-                ok = ok && mbar_wait(&sm.p_ready[j & 1], (unsigned)(j >> 1) & 1u);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t b = v_lo + (uint32_t)(j % kStages) * (kTileBytes >> 4), d = tmem + kOCol + kD * (j & 1);
-#pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    const uint32_t a = desc_lo(smem_u32(sm.p[j & 1][term]), 16);
-                    if (term == 0 && fresh) mma_f8<false>(d, a, kRowsHi, b, kKvHi, kIdescO);
-                    else mma_f8<true>(d, a, kRowsHi, b, kKvHi, kIdescO);
-                    mma_f8<true>(d, a + (32 >> 4), kRowsHi, b + (4 * kRegBytes >> 4), kKvHi, kIdescO);
-                }
-                umma_commit(&sm.empty[j % kStages]);
-                umma_commit(&sm.pv_done[j & 1]);
-            };
             while (u0 < n_q && ok) {
                 const Run r = run_at(sm, p, u0, u0 < single_until);
-                for (int ti = 0; ti < min(2, r.tiles); ++ti) issue_s(tg + ti);
                 for (int ti = 0; ti < r.tiles && ok; ++ti, ++tg) {
-                    if (ti + 2 < r.tiles) {
-                        ok = ok && mbar_wait(&sm.s_read[tg & 1], (unsigned)(tg >> 1) & 1u);
-                        if (ok) issue_s(tg + 2);
-                    }
-                    issue_pv(tg, ti < 2);
+                    const int st = tg % kStages;
+                    ok = mbar_wait(&sm.full[st], (unsigned)(tg / kStages) & 1u) &&
+                         (ti < 2 || mbar_wait(&sm.s_read[tg & 1], (unsigned)((tg - 2) >> 1) & 1u));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t b = k_lo + (uint32_t)st * (kTileBytes >> 4), d = tmem + 64 * (tg & 1);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int ks = 0; ks < 6; ++ks) {
+                            const uint32_t a = desc_lo(smem_u32(sm.q[term]) + (ks >> 1) * 8192 + (ks & 1) * 32, 16);
+                            const uint32_t bk = b + (((ks >> 1) * 1024 + (ks & 1) * 32) >> 4);
+                            if (term == 0 && ks == 0) mma_f8<false>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                            else mma_f8<true>(d, a, kRowsHi, bk, kKvHi, kIdescS);
+                        }
+                    umma_commit(&sm.s_full[tg & 1]);
                 }
                 if (ok) mbar_arrive(&sm.run_done);
                 ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
                 next(r);
             }
             // no MMA is in flight when TMEM is released, after a wait that gave up as well
+            umma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0u);
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- O += P' V as the weights are there (one lane).  V^T: 64-dim blocks 1 KiB apart, 8-token
+        // groups 3 KiB apart; P': rows of 64 bytes
+        if (lane == 0) {
+            const uint32_t v_lo = desc_lo(smem_u32(ring) + 512, 1024);
+            constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
+            while (u0 < n_q && ok) {
+                const Run r = run_at(sm, p, u0, u0 < single_until);
+                for (int ti = 0; ti < r.tiles && ok; ++ti, ++tg) {
+                    ok = mbar_wait(&sm.p_ready[tg & 1], (unsigned)(tg >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t b = v_lo + (uint32_t)(tg % kStages) * (kTileBytes >> 4), d = tmem + kOCol + kD * (tg & 1);
+#pragma unroll
+                    for (int term = 0; term < 3; ++term) {
+                        const uint32_t a = desc_lo(smem_u32(sm.p[tg & 1][term]), 16);
+                        if (term == 0 && ti < 2) mma_f8<false>(d, a, kRowsHi, b, kKvHi, kIdescO);
+                        else mma_f8<true>(d, a, kRowsHi, b, kKvHi, kIdescO);
+                        mma_f8<true>(d, a + (32 >> 4), kRowsHi, b + (4 * kRegBytes >> 4), kKvHi, kIdescO);
+                    }
+                    umma_commit(&sm.empty[tg % kStages]);
+                    umma_commit(&sm.pv_done[tg & 1]);
+                }
+                if (ok) mbar_arrive(&sm.run_done);
+                ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
+                next(r);
+            }
             umma_commit(&sm.drain);
             mbar_wait(&sm.drain, 0u);
         }
@@ -385,45 +393,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.s_read[grp]);
-                float mx = -INFINITY, mv = -INFINITY;
-                if (whole && __all_sync(0xffffffffu, mine)) {
+                // a score is s[i] fr, fr = qf times K's scale where the whole warp attends the whole tile; else
+                // the scores themselves (-inf: not attended) take the place of s and fr is 1
+                const bool plain = whole && __all_sync(0xffffffffu, mine);
+                if (!plain) {
 #pragma unroll
                     for (int rg = 0; rg < 8; ++rg) {
-                        const float4 sc = sm.scale[st][rg];
-                        const float f = qf * sc.x;
-                        float y = -INFINITY;
-#pragma unroll
-                        for (int i = 8 * rg; i < 8 * rg + 8; ++i) {
-                            s[i] *= f;
-                            y = fmaxf(y, s[i]);
-                        }
-                        mx = fmaxf(mx, y);
-                        mv = fmaxf(mv, y + sc.z);
-                    }
-                } else {
-#pragma unroll
-                    for (int rg = 0; rg < 8; ++rg) {
-                        const float4 sc = sm.scale[st][rg];
-                        const float f = qf * sc.x;
-                        float y = -INFINITY;
+                        const float f = qf * sm.scale[st][rg].x;
 #pragma unroll
                         for (int i = 8 * rg; i < 8 * rg + 8; ++i) {
                             const int t = t0 + i;
                             s[i] = there && t >= t_lo && t <= pos ? s[i] * f : -INFINITY;
-                            y = fmaxf(y, s[i]);
                         }
-                        mx = fmaxf(mx, y);
-                        mv = fmaxf(mv, y + sc.z);
                     }
+                }
+                float mx = -INFINITY, mv = -INFINITY;
+#pragma unroll
+                for (int rg = 0; rg < 8; ++rg) {
+                    const float4 sc = sm.scale[st][rg];
+                    const float *x = s + 8 * rg;
+                    float y = fmaxf(fmaxf(x[0], x[1]), x[2]);
+                    y = fmaxf(fmaxf(y, x[3]), x[4]);
+                    y = fmaxf(fmaxf(y, x[5]), x[6]);
+                    y = fmaxf(y, x[7]) * (plain ? qf * sc.x : 1.0f);
+                    mx = fmaxf(mx, y);
+                    mv = fmaxf(mv, y + sc.z);
                 }
                 // this group's tile before (tg - 2) is in O, and its P' has been read
                 if (ti >= 2) wait(&sm.pv_done[grp], (unsigned)((tg - 2) >> 1) & 1u);
                 __syncwarp();
                 // the references move where a token passes one by more than the slack, or there is none
-                const bool grow = mx > m + kSlack || mv > M + kSlack || (M == -INFINITY && mx > -INFINITY);
-                if (__any_sync(0xffffffffu, grow)) {
+                const bool move = mx > m + kSlack || mv > M + kSlack || (M == -INFINITY && mx > -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
                     float al = 1.0f, ao = 1.0f;
-                    if (grow) {
+                    if (move) {
                         const float a = fmaxf(m, mx), d = fmaxf(M, mv);
                         if (a != m) al = exp2f(m - a);
                         if (d != M) ao = exp2f(M - d);
@@ -436,16 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ti >= 2 && __any_sync(0xffffffffu, ao != 1.0f)) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kD; c0 += 64) {
-                            float o[32], o2[32];
-                            tmem_ld32x2(tcol_o + c0, tcol_o + c0 + 32, o, o2);
+                        for (int c0 = 0; c0 < kD; c0 += 32) {
+                            float o[32];
+                            tmem_ld32(tcol_o + c0, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                o[i] *= ao;
-                                o2[i] *= ao;
-                            }
+                            for (int i = 0; i < 32; ++i) o[i] *= ao;
                             tmem_st32(tcol_o + c0, o);
-                            tmem_st32(tcol_o + c0 + 32, o2);
                         }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tc_fence_before();
@@ -454,18 +453,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P' in three e5m2 terms: the upper bytes of w, of what they leave, and of the rest,
                 // rounded; 16 tokens at a time
                 uint8_t *dst = sm.p[grp][0] + row * 64;
+                float2 add2 = make_float2(0.0f, 0.0f);
+                const float2 mr2 = make_float2(-mref, -mref), one2 = make_float2(1.0f, 1.0f);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     uint32_t w[8];
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float f = fminf(sm.scale[st][2 * ch + hf].y * c, 8.5070592e37f);     // 2^126
+                        const float4 sc = sm.scale[st][2 * ch + hf];
+                        const float fr = plain ? qf * sc.x : 1.0f, f = fminf(sc.y * c, 8.5070592e37f);     // 2^126
+                        const float2 fr2 = make_float2(fr, fr), f2 = make_float2(f, f);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int e = 16 * ch + 8 * hf + 2 * i;
-                            const float p0 = ex2(s[e] - mref), p1 = ex2(s[e + 1] - mref);
-                            l += p0 + p1;
-                            w[4 * hf + i] = attnq::pack_f16x2(p0 * f, p1 * f);
+                            const float2 x = ffma2(make_float2(s[e], s[e + 1]), fr2, mr2);
+                            const float2 p2 = make_float2(ex2(x.x), ex2(x.y));
+                            add2 = ffma2(p2, one2, add2);
+                            const float2 y = fmul2(p2, f2);
+                            w[4 * hf + i] = attnq::pack_f16x2(y.x, y.y);
                         }
                     }
                     const int at = (ch ^ ((row >> 1) & 3)) << 4;
@@ -484,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                l += add2.x + add2.y;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_ready[grp]);
