@@ -109,10 +109,6 @@ dsa_status_t group_range_args(int g0, int ng)
 }
 
 constexpr int kGemmMinQueries = 64;   // FP8 prefill chunks at least this long use the GEMM
-// Quantised window calls at least this long share neighbours' windows.  Both sides measured: 128
-// queries 28.8 us row by row and 29.6 shared (window 512), 11.4 and 17.3 (64), 43.5 and 41.2 (1,024);
-// 256 queries 53.7 and 30.4, 21.0 and 17.8, 82.4 and 42.5.
-constexpr int kBandMinQueries = 192;
 constexpr int kSharedMinQueries = 32; // prefill attention calls at least this long share selections
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1265,9 +1261,12 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     p.k = k;
     p.window = window;
     p.scale_log2 = dsa::attnq::kLog2e / sqrtf((float)dsa::kD);
-    // chunks: 8 neighbouring queries of the list share their windows' tokens, where a request has at
-    // least that many queries on average (a decode list's neighbours are different requests)
-    if (window > 0 && nq >= kBandMinQueries && nq >= 8 * (int64_t)n_req) {
+    // Chunks: 8 neighbouring queries of the list share their windows' tokens, where a request has at
+    // least that many queries on average (a decode list's neighbours are different requests) and the
+    // rows are more than one round of CTAs (windows below 128: two).  Shared / row by row, us: 74
+    // queries 15.3 / 10.3 (window 128), 17.5 / 12.5 (256); 80 queries 22.2 / 27.3 (512), 31.3 / 35.3
+    // (1,024); 128 queries 15.6 / 16.5 (128), 13.6 / 11.5 (64); 160 queries 13.9 / 15.7 (64).
+    if (window > 0 && nq >= 8 * (int64_t)n_req && (int64_t)nq * dsa::kG > resident * (window < 128 ? 2 : 1)) {
         const int blocks = (nq + dsa::attnqb::kQueries - 1) / dsa::attnqb::kQueries * dsa::kG;
         return launch_k("window_attn_band_kernel", dsa::attnqb::window_attn_band_kernel, dim3((unsigned)blocks),
                         dim3(dsa::attnqb::kThreads), dsa::attnqb::kSmemBytes, stream, 0, map, p);
