@@ -76,11 +76,20 @@ __global__ void __launch_bounds__(256) kv_append_quant_kernel(
         if (((after >> (len - 1)) & 1u) && threadIdx.x == 0) set_error(kErrAppendOrder);
         const int p0 = __shfl_sync(0xffffffffu, pos, l0), b = __shfl_sync(0xffffffffu, req, l0);
         const unsigned rows = __reduce_or_sync(0xffffffffu, lane >= l0 && lane < l0 + len ? 1u << (pos & 7) : 0u);
-        if (b < 0 || b >= n_req || p0 < 0 || p0 / kPage >= max_pages) {
-            if (threadIdx.x == 0) set_error(kErrAttnIndex);
-            continue;
+        const bool in_table = b >= 0 && b < n_req && p0 >= 0 && p0 / kPage < max_pages;
+        const int64_t page = in_table ? block_table[(int64_t)b * max_pages + p0 / kPage] : -1;
+        // (the new rows travel while the page is looked up)
+        // chunk c = lane + 32 u: row c / 24 of the region, its elements 8 (c % 24) .. + 7
+        uint4 x[6];
+#pragma unroll
+        for (int u = 0; u < 6; ++u) {
+            const int c = lane + 32 * u, r = c / 24, cc = c % 24;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if ((rows >> r) & 1u) {
+                const int64_t i = i0 - 1 + l0 + __popc(rows & ((1u << r) - 1u));
+                x[u] = __ldg(reinterpret_cast<const uint4 *>(src + (i * kG + g) * kD + cc * 8));
+            }
         }
-        const int64_t page = block_table[(int64_t)b * max_pages + p0 / kPage];
         if (page < 0 || page >= n_pages) {
             if (threadIdx.x == 0) set_error(kErrAttnIndex);
             continue;
@@ -90,21 +99,13 @@ __global__ void __launch_bounds__(256) kv_append_quant_kernel(
         float *sp = scale + rid * 2 + which;
         const int first = __ffs(rows) - 1;                                  // rows below it are kept
         const float s_old = first > 0 ? *sp : 0.0f;
-        // chunk c = lane + 32 u: row c / 24 of the region, its elements 8 (c % 24) .. + 7
-        uint4 x[6];
         uint2 old[6];
         __nv_bfloat162 mx2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
         for (int u = 0; u < 6; ++u) {
             const int c = lane + 32 * u, r = c / 24, cc = c % 24;
-            x[u] = make_uint4(0, 0, 0, 0);
             old[u] = make_uint2(0, 0);
-            if ((rows >> r) & 1u) {
-                const int64_t i = i0 - 1 + l0 + __popc(rows & ((1u << r) - 1u));
-                x[u] = __ldg(reinterpret_cast<const uint4 *>(src + (i * kG + g) * kD + cc * 8));
-            } else if (r < first) {
-                old[u] = *reinterpret_cast<const uint2 *>(block + r * kD + cc * 8);
-            }
+            if (r < first) old[u] = *reinterpret_cast<const uint2 *>(block + r * kD + cc * 8);
         }
 #pragma unroll
         for (int u = 0; u < 6; ++u) {

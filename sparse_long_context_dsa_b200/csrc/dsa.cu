@@ -1326,9 +1326,11 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
     if ((st = device_info(sms)) != DSA_OK) return st;
     const int rows = q_req ? n_req : n;
     const __nv_bfloat16 *nk = static_cast<const __nv_bfloat16 *>(new_k), *nv = static_cast<const __nv_bfloat16 *>(new_v);
-    // one list entry per CTA while that fills the GPU less than twice over (a decode step's runs
-    // are single tokens, and 8 of them in one CTA would wait for one another), else 8
-    if (n <= 2 * 8 * sms)
+    // One list entry per CTA, or 8 (one run, as a rule) for long chunks, where most CTAs of one entry
+    // hold no run's first.  us with 1 / 8: a chunk of 64 tokens 2.7 / 3.6, 512 3.6 / 3.7, 1,024 4.6 / 4.0,
+    // 2,048 5.9 / 4.1; a decode step's runs are single tokens, and 8 of them in one CTA wait for one
+    // another: 8 requests 2.7 / 10.4, 1,024 7.5 / 13.3, 4,096 27.5 / 30.6.
+    if (!q_req || n < 8 * (int64_t)n_req || n <= 4 * sms)
         return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<1>, dim3((unsigned)n), dim3(256), 0,
                         stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n, nk, nv);
     return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<8>, dim3((unsigned)((n + 7) / 8)),

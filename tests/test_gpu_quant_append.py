@@ -70,6 +70,35 @@ def test_ragged_requests_in_one_call():
     dsa.check_device()
 
 
+def test_ragged_requests_in_a_long_call():
+    # runs of any length at any offset, at every place of 8 list entries; some entries skipped
+    counts = [333, 1, 0, 95, 7, 410, 130]
+    starts = [70, 3, 0, 61, 6, 5, 64]
+    pages = sum((s + c + 63) // 64 for s, c in zip(starts, counts)) + 1
+    table = Q.random_table([s + c for s, c in zip(starts, counts)], pages, 15)
+    keep = [i for i in range(sum(counts)) if i % 41 not in (3, 17)]
+    req = [b for b, c in enumerate(counts) for _ in range(c)]
+    pos = [s + j for s, c in zip(starts, counts) for j in range(c)]
+    req, pos = [req[i] for i in keep], [pos[i] for i in keep]
+    cache, scale = Q.filled_cache(pages, 16)
+    run(cache, scale, table, req, pos, *new_rows(len(req), 17))
+    dsa.check_device()
+    # entries of two bad pages among the others
+    bad = np.array(table)
+    bad[0, 3], bad[5, 4] = pages, -1
+    x, y = new_rows(len(req), 18)
+    c, s = cache.cuda(), scale.cuda()
+    i32 = lambda v: torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")
+    dsa.kv_append_quant(c, s, i32(bad), i32(pos), x.cuda(), y.cuda(), q_req=i32(req))
+    with pytest.raises(dsa.DsaError):
+        dsa.check_device()
+    good = [i for i in range(len(req)) if (req[i], pos[i] // 64) not in ((0, 3), (5, 4))]
+    assert 0 < len(good) < len(req)
+    wc, ws = Q.append(cache.numpy(), scale.double().numpy(), bad, [req[i] for i in good], [pos[i] for i in good],
+                      x[good].double().numpy(), y[good].double().numpy())
+    assert np.array_equal(c.cpu().numpy(), wc) and np.array_equal(s.cpu().double().numpy(), ws)
+
+
 def test_rows_of_a_run_may_leave_gaps():
     cache, scale = Q.filled_cache(2, 8)
     run(cache, scale, [[1, 0]], [0, 0, 0, 0], [1, 3, 6, 66], *new_rows(4, 9))
