@@ -386,8 +386,8 @@ dsa_status_t dsa_sparse_attn_decode_groups(const void *q, const void *k_cache, c
  * a token is appended again after a rollback before it is attended.  Infinities saturate and
  * take their block's scale to 2^120; NaN stays NaN and leaves the scale to the other values.  A
  * q_req outside [0, n_req), a position that is negative or beyond the block table, a page
- * outside [0, n_pages) and an entry that does not ascend in its run are skipped and flag
- * DSA_ERR_DEVICE. */
+ * outside [0, n_pages), and in a run an entry that does not ascend with those behind it, are skipped
+ * and flag DSA_ERR_DEVICE. */
 dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_pages, const int32_t *block_table,
                                  int max_pages, int n_req, const int32_t *q_req, const int32_t *q_pos, int n,
                                  const void *new_k, const void *new_v, dsa_stream_t stream);
@@ -397,7 +397,7 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
  * their arguments, results and errors (nq <= 2^24, out 8-byte aligned; a query at a negative
  * position attends nothing: out = 0, lse = -inf).  Scales are finite and >= 0, powers of two or not.
  * Scores and sums are fp32; q enters the products as two e4m3 terms (off by at most 2^-18 of the
- * head's largest element), the softmax weights as fp16.  Tokens outside a query's T may hold any
+ * head's largest element; infinities saturate), the softmax weights as fp16.  Tokens outside a query's T may hold any
  * bytes, NaN codes among them.  The results do not depend on the other queries of the call.  No
  * workspace. */
 dsa_status_t dsa_sparse_attn_decode_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
@@ -420,11 +420,11 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
  * paged cache, without a host synchronisation).  ref int32 [n_pages] counts the table entries that
  * hold a page (0 or less: free); block_table int32 [n_req][max_pages], -1 where a request has no
  * page.  Every call reads ref_in and table_in and leaves its result, whole, in ref_out and table_out;
- * an output may be its input itself (in place) but not overlap it otherwise.  An allocation takes
- * the lowest free pages, so results are functions of the arguments alone.  n <= 4096,
+ * an output may be its input itself (in place); no other arrays of a call overlap.  An allocation
+ * takes the lowest free pages, so results are functions of the arguments alone.  n <= 4096,
  * max_pages < 2^31 / 64.  A pool is an array [n_pages] of pages of page_bytes (a multiple of 16,
  * 16-byte aligned): the caches of every layer that share a block table, with their scales.
- * `pools` is a host array, read during the call; pools must not overlap one another.
+ * `pools` is a host array, read during the call.
  *
  * dsa_pages_fork: for i = 0 .. n - 1, row child[i] becomes a request of the first length[i] tokens
  *   of row parent[i]: it shares the full pages (their counts rise) and, for a partly filled last

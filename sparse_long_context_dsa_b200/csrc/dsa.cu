@@ -1370,6 +1370,12 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
 namespace {
 constexpr int kMaxListed = 4096;      // forks or releases of one call (each looks at the others)
 
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 dsa_status_t page_table_args(const int32_t *ref_in, const int32_t *ref_out, int64_t n_pages, const int32_t *table_in,
                              const int32_t *table_out, int max_pages, int n_req)
 {
@@ -1379,14 +1385,16 @@ dsa_status_t page_table_args(const int32_t *ref_in, const int32_t *ref_out, int6
     DSA_REQUIRE(ref_in && ref_out && table_in && table_out, "NULL pointer");
     DSA_REQUIRE(aligned(ref_in, 4) && aligned(ref_out, 4) && aligned(table_in, 4) && aligned(table_out, 4),
                 "misaligned pointer");
-    const auto overlap = [](const int32_t *a, const int32_t *b, int64_t n) { return a != b && a < b + n && b < a + n; };
-    DSA_REQUIRE(!overlap(ref_in, ref_out, n_pages) && !overlap(table_in, table_out, (int64_t)n_req * max_pages),
+    const int64_t r = n_pages * 4, t = (int64_t)n_req * max_pages * 4;
+    DSA_REQUIRE((ref_in == ref_out || !overlap(ref_in, r, ref_out, r)) &&
+                    (table_in == table_out || !overlap(table_in, t, table_out, t)),
                 "an output may be its input itself, but not overlap it");
-    DSA_REACHABLE({ref_in, "ref_in"}, {ref_out, "ref_out"}, {table_in, "table_in"}, {table_out, "table_out"});
+    DSA_REQUIRE(!overlap(ref_out, r, table_in, t) && !overlap(ref_out, r, table_out, t) && !overlap(ref_in, r, table_out, t),
+                "the counts and the table overlap");
     return DSA_OK;
 }
 
-dsa_status_t page_pools(const dsa_page_pool_t *pools, int n_pools, dsa::pages::Pools &out)
+dsa_status_t page_pools(const dsa_page_pool_t *pools, int n_pools, int64_t n_pages, dsa::pages::Pools &out)
 {
     DSA_REQUIRE(n_pools >= 0 && n_pools <= DSA_MAX_PAGE_POOLS, "n_pools out of [0, DSA_MAX_PAGE_POOLS]");
     DSA_REQUIRE(n_pools == 0 || pools, "NULL pointer");
@@ -1397,6 +1405,9 @@ dsa_status_t page_pools(const dsa_page_pool_t *pools, int n_pools, dsa::pages::P
         DSA_REQUIRE(aligned(pools[i].data, 16) && pools[i].page_bytes >= 16 && pools[i].page_bytes % 16 == 0 &&
                         pools[i].page_bytes <= (1ll << 32),
                     "a pool must be 16-byte aligned, its page a multiple of 16 bytes and at most 2^32");
+        for (int j = 0; j < i; ++j)
+            DSA_REQUIRE(!overlap(pools[i].data, n_pages * pools[i].page_bytes, pools[j].data, n_pages * pools[j].page_bytes),
+                        "pools overlap");
         DSA_REACHABLE({pools[i].data, "pool"});
         out.data[i] = static_cast<uint8_t *>(pools[i].data);
         out.bytes[i] = pools[i].page_bytes;
@@ -1443,8 +1454,9 @@ dsa_status_t dsa_pages_fork(const int32_t *ref_in, int32_t *ref_out, int64_t n_p
     if (st != DSA_OK) return st;
     DSA_REQUIRE(n == 0 || (parent && child && length), "NULL pointer");
     dsa::pages::Pools pp;
-    if ((st = page_pools(pools, n_pools, pp)) != DSA_OK) return st;
-    DSA_REACHABLE({parent, "parent"}, {child, "child"}, {length, "length"}, {ws, "ws"});
+    if ((st = page_pools(pools, n_pools, n_pages, pp)) != DSA_OK) return st;
+    DSA_REACHABLE({ref_in, "ref_in"}, {ref_out, "ref_out"}, {table_in, "table_in"}, {table_out, "table_out"},
+                  {parent, "parent"}, {child, "child"}, {length, "length"}, {ws, "ws"});
     const size_t need = dsa_pages_fork_workspace_size(n);
     if (n > 0 && (!ws || ws_bytes < need || !aligned(ws, 256)))
         return fail(DSA_ERR_WORKSPACE, "fork workspace too small or not 256-byte aligned (need " + std::to_string(need) +
@@ -1483,7 +1495,8 @@ dsa_status_t dsa_pages_release(const int32_t *ref_in, int32_t *ref_out, int64_t 
     dsa_status_t st = page_table_args(ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req);
     if (st != DSA_OK) return st;
     DSA_REQUIRE(n == 0 || (req && keep), "NULL pointer");
-    DSA_REACHABLE({req, "req"}, {keep, "keep"});
+    DSA_REACHABLE({ref_in, "ref_in"}, {ref_out, "ref_out"}, {table_in, "table_in"}, {table_out, "table_out"},
+                  {req, "req"}, {keep, "keep"});
     int sms = 0;
     if ((st = device_info(sms)) != DSA_OK) return st;
     const int64_t table_n = (int64_t)n_req * max_pages;
@@ -1509,9 +1522,17 @@ dsa_status_t dsa_pages_compact(const int32_t *ref_in, int32_t *ref_out, int64_t 
     dsa_status_t st = page_table_args(ref_in, ref_out, n_pages, table_in, table_out, max_pages, n_req);
     if (st != DSA_OK) return st;
     DSA_REQUIRE(new_index && n_live, "NULL pointer");
-    DSA_REACHABLE({new_index, "new_index"}, {n_live, "n_live"}, {ws, "ws"});
+    {
+        const int64_t r = n_pages * 4, t = (int64_t)n_req * max_pages * 4;
+        for (const auto &o : {std::pair<const void *, int64_t>{ref_in, r}, {ref_out, r}, {table_in, t}, {table_out, t}})
+            DSA_REQUIRE(!overlap(new_index, r, o.first, o.second) && !overlap(n_live, 4, o.first, o.second),
+                        "new_index and n_live are arrays of their own: they overlap others");
+        DSA_REQUIRE(!overlap(new_index, r, n_live, 4), "new_index and n_live are arrays of their own: they overlap");
+    }
+    DSA_REACHABLE({ref_in, "ref_in"}, {ref_out, "ref_out"}, {table_in, "table_in"}, {table_out, "table_out"},
+                  {new_index, "new_index"}, {n_live, "n_live"}, {ws, "ws"});
     dsa::pages::Pools pp;
-    if ((st = page_pools(pools, n_pools, pp)) != DSA_OK) return st;
+    if ((st = page_pools(pools, n_pools, n_pages, pp)) != DSA_OK) return st;
     const size_t need = dsa_pages_compact_workspace_size(n_pages);
     if (!ws || ws_bytes < need || !aligned(ws, 256))
         return fail(DSA_ERR_WORKSPACE, "compact workspace too small or not 256-byte aligned (need " +

@@ -290,6 +290,17 @@ def test_a_large_page_and_offsets_behind_four_gigabytes():
     assert int(n_live) == pages - 1 and int(to[0, 0]) == 7 and torch.equal(pool[7], row.to(torch.uint8))
 
 
+def test_pools_that_overlap_are_refused():
+    ref, table = torch.zeros(8, dtype=torch.int32, device="cuda"), i32([[-1, -1]] * 2)
+    data = torch.zeros(9 * 64, dtype=torch.uint8, device="cuda")
+    a, b = data[:512].view(8, 64), data[64:].view(8, 64)
+    for pools in ([a, b], [a, a]):
+        with pytest.raises(dsa.DsaError, match="overlap"):
+            dsa.pages_compact(ref, table, pools)
+        with pytest.raises(dsa.DsaError, match="overlap"):
+            dsa.pages_fork(ref, table, i32([0]), i32([1]), i32([0]), pools)
+
+
 def test_streams_and_graphs():
     ref, table, pools = pool_of([300, 500], 60, 10, rows=5)
     want = fork(ref, table, [0, 1, 1], [2, 3, 4], [290, 400, 500], pools)

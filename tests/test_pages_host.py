@@ -5,7 +5,7 @@ import torch
 from sparse_long_context_dsa_b200 import build as B
 from sparse_long_context_dsa_b200 import dsa
 
-P = 1 << 20                        # an address that is never read: these calls return before any device access
+P, Q = 1 << 20, 1 << 22            # addresses that are never read: these calls return before any device access
 
 
 @pytest.fixture(scope="module")
@@ -50,3 +50,17 @@ def test_the_binding_refuses_other_shapes_and_host_tensors():
         dsa.pages_compact(ref, table, [torch.zeros((4, 16))])
     with pytest.raises(ValueError):
         dsa.pages_fork(ref, table, one, one, one, [])
+
+
+@pytest.mark.parametrize("call,word", [
+    # the counts and the table in one array
+    (lambda L: L.dsa_pages_fork(P, P, 8, P + 16, P + 16, 3, 2, Q, Q, Q, 1, None, 0, None, 0, None), "overlap"),
+    (lambda L: L.dsa_pages_release(P, P + 64, 8, P + 512, P + 80, 3, 2, Q, Q, 1, None), "overlap"),
+    # what a compaction returns in place of what it reads
+    (lambda L: L.dsa_pages_compact(P, P, 8, P + 512, P + 512, 3, 2, P, Q, None, 0, None, 0, None), "overlap"),
+    (lambda L: L.dsa_pages_compact(P, P, 8, P + 512, P + 512, 3, 2, Q, P + 512, None, 0, None, 0, None), "overlap"),
+    (lambda L: L.dsa_pages_compact(P, P, 8, P + 512, P + 512, 3, 2, Q, Q + 28, None, 0, None, 0, None), "overlap"),
+])
+def test_arrays_that_overlap_are_refused(lib, call, word):
+    assert call(lib) == dsa.ERR_INVALID_ARG
+    assert word in lib.dsa_last_error().decode()
