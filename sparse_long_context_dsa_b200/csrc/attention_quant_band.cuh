@@ -52,7 +52,7 @@ struct Smem {
     int pos[kQueries], req[kQueries];
     int run_end[kQueries];                                       // first query behind the run that begins here
     int nan[2];                                                  // run n (by parity) met a NaN code at a partly attended token: n + 1
-    uint64_t full[kStages], empty[kStages], s_full[2], s_read[2], p_ready[2], pv_done[2], merged, run_done, drain;
+    uint64_t full[kStages], empty[kStages], s_full[2], s_read[2], p_ready[2], pv_done[2], merged, run_done, drain[2];
     uint32_t tmem;
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&sm.merged, 8);
         mbar_init(&sm.run_done, 11);                             // every role: none is two runs behind another
-        mbar_init(&sm.drain, 2);
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
         sm.nan[0] = sm.nan[1] = 0;
         fence_mbar_init();
     }
@@ -293,8 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next(r);
             }
             // no MMA is in flight when TMEM is released, after a wait that gave up as well
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0u);
+            if (ok) {
+                if (tg > 0) mbar_wait(&sm.s_full[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
+            } else {
+                umma_commit(&sm.drain[0]);
+                mbar_wait(&sm.drain[0], 0u);
+            }
         }
         __syncwarp();
     } else if (warp == 10) {
@@ -324,8 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
                 next(r);
             }
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0u);
+            if (ok) {
+                if (tg > 0) mbar_wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
+            } else {
+                umma_commit(&sm.drain[1]);
+                mbar_wait(&sm.drain[1], 0u);
+            }
         }
         __syncwarp();
     } else {

@@ -350,9 +350,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     ok = false;
                 }
             }
-            // no MMA is in flight when TMEM is released, after a wait that gave up as well
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0u);
+            // no MMA is in flight when TMEM is released: the last tile's commit covers all of them.  (A commit
+            // of its own here, on the heels of a P' V of one step, now and then never returned; it is left
+            // to the case of a wait that gave up.)
+            if (ok) {
+                if (j > 0) mbar_wait(&sm.pv_done, (unsigned)(j - 1) & 1u);
+            } else {
+                umma_commit(&sm.drain);
+                mbar_wait(&sm.drain, 0u);
+            }
         }
         __syncwarp();
     } else {

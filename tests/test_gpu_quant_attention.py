@@ -168,6 +168,25 @@ def test_window_decode(w):
     Q.check_attention(out, lse, reference(cache, scale, table, q, range(len(pos)), pos, Q.window_tokens(pos, w)))
 
 
+@pytest.mark.parametrize("batch,w", [(8, 512), (8, 520), (1, 9), (3, 64), (40, 100)])
+def test_many_short_calls_in_a_row(batch, w):
+    # calls of a few microseconds one behind another, their last tiles of one to four steps: every
+    # one of them ends, and the last gives what the first gave
+    pages = 12 * batch
+    table = np.arange(pages).reshape(batch, 12)
+    cache, scale = Q.filled_cache(pages, 301)
+    pos = [700 + i % 9 for i in range(batch)]
+    args = (Q.rows((batch, 64, 192), 302, 0.3).cuda(), cache.cuda(), scale.cuda(), to(table), to(pos), w)
+    first = dsa.window_attn_quant(*args)
+    out = torch.empty_like(first)
+    for i in range(20000):
+        dsa.window_attn_quant(*args, out=out)
+        if i % 1000 == 999:
+            torch.cuda.synchronize()
+    dsa.check_device()
+    assert torch.equal(out, first)
+
+
 def test_window_chunk_of_one_request():
     pages = 12
     table = Q.random_table([700], pages, 93)
