@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         // ---- S, at most two tiles ahead of the weights (one lane).  K: rows of 64 bytes, 8 of a region
         // 512 bytes, regions 3 KiB apart; q: rows of 64 bytes
-        if (lane == 0) {
+        if (attnqt::elect_one()) {
             const uint32_t k_lo = desc_lo(smem_u32(ring), 16);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
             while (u0 < n_q && ok) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 10) {
         // ---- O += P' V as the weights are there (one lane).  V^T: 64-dim blocks 1 KiB apart, 8-token
         // groups 3 KiB apart; P': rows of 64 bytes
-        if (lane == 0) {
+        if (attnqt::elect_one()) {
             const uint32_t v_lo = desc_lo(smem_u32(ring) + 512, 1024);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
             while (u0 < n_q && ok) {

@@ -1,4 +1,28 @@
-// (header comment written once the kernel is settled)
+// GQA of a (query, KV group) row over the 8-bit paged cache (layout and scales: append_quant.cuh):
+// its selected regions, or its window's.  With q, k, v the row's 16 queries and its tokens' values,
+//   s_t = q . k_t / sqrt(192),   out = sum_t e^(s_t) v_t / sum_t e^(s_t).
+//
+// Tiles of 16 regions (128 tokens, 48 KiB: a box {64 dims, 16 rows, 3 blocks} per region lands K's
+// and V's 8 rows as the MMAs take them).  tokens (S) and dims (O) are the MMA's M, the 16 heads
+// its N: a row has no more of them.
+//  * S^T = K q^T: kind::f8f6f4 straight from the codes, 6 steps of K = 32.  2^-e q = hi + lo / 16 in
+//    e4m3 side by side in N (off by at most 2^-18 of the head's largest element); the codes' scale
+//    and q's multiply the fp32 sums.
+//  * softmax: thread = token, fp32, log2 units, against references m (of s) and M (of s + log2 of V's
+//    scale) of each head that move only where a weight passes 2^15 (then O is rescaled in TMEM).
+//  * O^T += V^T P'^T: V's codes MN-major, P' = 2^(s - m) sV 2^(m - M) as three e5m2 terms (cut off, cut
+//    off, rounded) of its fp16 value, side by side in N; the terms are added at the end.
+// Rows of few queries are split over a cluster, whose CTAs' (O, m, M, l) meet in distributed shared
+// memory; many rows run through one CTA after another without draining the ring.
+// Warps: 0-3 softmax, 4 loads (the lookups of the next 32 regions run ahead), 5 the MMAs' issuer.
+//
+// Bound: a row's chain load - S - softmax - P' V - the next weights, with two CTAs per SM and two tiles
+// each in flight: of ~3,000 cycles a tile the weights take 900 and the P' V behind them 1,000.  k = 512:
+// one decode at 16,384 tokens 10.1 us (latency: 64 CTAs of two tiles), 8 at 131,072 19.4 us (2.6 TB/s), 32 of
+// 4,096 .. 262,144 47.4 us (4.3 TB/s, 0.66 of the copy rate), a chunk of 256 queries at 32,768 210 us (1.6 GB
+// of gathers from L2, 7.7 TB/s; with the issuer as lane 0 in place of an elected lane 229: tensor pipe
+// 17 %, issue slots 36 %).  Tried and not faster (the chunk, us against those 229): regions as boxes of 128 and 64 dims, two rows of a
+// token in place of three 243; K's and V's places released apart 236; eight softmax warps of 8 heads 238.
 #pragma once
 
 #include <type_traits>
@@ -61,6 +85,18 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi,
 constexpr uint32_t kIdescS = umma_idesc_e4m3(128, kN);
 // V^T (A, e4m3) and P'^T (B, e5m2) MN-major
 constexpr uint32_t kIdescO = umma_idesc_e4m3(128, kNp) | (1u << 10) | (1u << 15) | (1u << 16);
+
+// True in one lane of a whole warp.
+__device__ __forceinline__ bool elect_one()
+{
+    unsigned one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
 
 // Whether the phase of `bar` with the given parity is complete; never suspends.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned parity)
@@ -283,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         __syncwarp();
     } else if (warp == 5) {
-        // ---- MMA issuer (one lane): S(i) as its codes land, O += P'(j) V(j) as the weights are
+        // ---- MMA issuer (one elected lane): S(i) as its codes land, O += P'(j) V(j) as the weights are
         // there, whichever is ready; at most two S are ahead of the weights
-        if (lane == 0) {
+        if (elect_one()) {
             // K: rows of 64 bytes, a region's 8 rows 512 bytes, regions 3 KiB apart; V^T: 64-dim blocks
             // 1 KiB apart, 8-token groups 3 KiB apart; P'^T: 8 tokens x 16 heads 128 bytes, terms 2 KiB apart
             const uint32_t k_lo = desc_lo(smem_u32(ring), 16), v_lo = desc_lo(smem_u32(ring) + 512, 1024);
