@@ -52,7 +52,7 @@ struct Smem {
     int pos[kQueries], req[kQueries];
     int run_end[kQueries];                                       // first query behind the run that begins here
     int nan[2];                                                  // run n (by parity) met a NaN code at a partly attended token: n + 1
-    uint64_t full[kStages], empty[kStages], s_full[2], s_read[2], p_ready[2], pv_done[2], merged, run_done, drain[2];
+    uint64_t full[kStages], empty[kStages], s_full[2], s_read[2], p_ready[2], pv_done[2], merged, run_done;
     uint32_t tmem;
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kTileBytes + sizeof(Smem);
@@ -117,8 +117,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&sm.merged, 8);
         mbar_init(&sm.run_done, 11);                             // every role: none is two runs behind another
-        mbar_init(&sm.drain[0], 1);
-        mbar_init(&sm.drain[1], 1);
         sm.nan[0] = sm.nan[1] = 0;
         fence_mbar_init();
     }
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         // ---- S, at most two tiles ahead of the weights (one lane).  K: rows of 64 bytes, 8 of a region
         // 512 bytes, regions 3 KiB apart; q: rows of 64 bytes
-        if (attnqt::elect_one()) {
+        if (elect_one()) {
             const uint32_t k_lo = desc_lo(smem_u32(ring), 16);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
             while (u0 < n_q && ok) {
@@ -293,19 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
                 next(r);
             }
-            // no MMA is in flight when TMEM is released, after a wait that gave up as well
-            if (ok) {
-                if (tg > 0) mbar_wait(&sm.s_full[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
-            } else {
-                umma_commit(&sm.drain[0]);
-                mbar_wait(&sm.drain[0], 0u);
-            }
+            // every commit has arrived when TMEM is released, after a wait that gave up as well (umma_commit)
+            for (int b = 0; b < 2; ++b) commits_done(&sm.s_full[b], (tg + 1 - b) / 2);
         }
         __syncwarp();
     } else if (warp == 10) {
         // ---- O += P' V as the weights are there (one lane).  V^T: 64-dim blocks 1 KiB apart, 8-token
         // groups 3 KiB apart; P': rows of 64 bytes
-        if (attnqt::elect_one()) {
+        if (elect_one()) {
             const uint32_t v_lo = desc_lo(smem_u32(ring) + 512, 1024);
             constexpr uint32_t kKvHi = desc_hi(kRegBytes, 4), kRowsHi = desc_hi(512, 4);
             while (u0 < n_q && ok) {
@@ -329,12 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && mbar_wait(&sm.run_done, (unsigned)n_run & 1u);
                 next(r);
             }
-            if (ok) {
-                if (tg > 0) mbar_wait(&sm.pv_done[(tg - 1) & 1], (unsigned)((tg - 1) >> 1) & 1u);
-            } else {
-                umma_commit(&sm.drain[1]);
-                mbar_wait(&sm.drain[1], 0u);
-            }
+            for (int b = 0; b < 2; ++b) commits_done(&sm.pv_done[b], (tg + 1 - b) / 2);
+            for (int s = 0; s < kStages; ++s) commits_done(&sm.empty[s], (tg + kStages - 1 - s) / kStages);
         }
         __syncwarp();
     } else {

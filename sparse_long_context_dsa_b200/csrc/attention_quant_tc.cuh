@@ -56,7 +56,7 @@ struct Smem {
     int region[kStages][kTileRegions];                           // -1: none
     float qscale[16], mref[16], c[16], al[16], ao[16], m[16], M[16], f[16];
     float red[4][32];
-    uint64_t full[kStages], empty[kStages], s_full[2], p_ready, pv_done, q_ready, drain, inbox_bar;
+    uint64_t full[kStages], empty[kStages], s_full[2], p_ready, pv_done, q_ready, inbox_bar;
     uint32_t tmem;
     int state;                                                   // 1: some head has no V yet; 2: O is rescaled
 };
@@ -85,18 +85,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi,
 constexpr uint32_t kIdescS = umma_idesc_e4m3(128, kN);
 // V^T (A, e4m3) and P'^T (B, e5m2) MN-major
 constexpr uint32_t kIdescO = umma_idesc_e4m3(128, kNp) | (1u << 10) | (1u << 15) | (1u << 16);
-
-// True in one lane of a whole warp.
-__device__ __forceinline__ bool elect_one()
-{
-    unsigned one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one != 0;
-}
 
 // Whether the phase of `bar` with the given parity is complete; never suspends.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned parity)
@@ -234,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         mbar_init(&sm.p_ready, 1);
         mbar_init(&sm.pv_done, 1);
         mbar_init(&sm.q_ready, 4);
-        mbar_init(&sm.drain, 1);
         mbar_init(&sm.inbox_bar, 1);
         mbar_arrive_expect_tx(&sm.inbox_bar, (unsigned)(kHeadsPerGroup * kInRow * 4));
         fence_mbar_init();
@@ -386,15 +373,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     ok = false;
                 }
             }
-            // no MMA is in flight when TMEM is released: the last tile's commit covers all of them.  (A commit
-            // of its own here, on the heels of a P' V of one step, now and then never returned; it is left
-            // to the case of a wait that gave up.)
-            if (ok) {
-                if (j > 0) mbar_wait(&sm.pv_done, (unsigned)(j - 1) & 1u);
-            } else {
-                umma_commit(&sm.drain);
-                mbar_wait(&sm.drain, 0u);
-            }
+            // every commit has arrived when TMEM is released, after a wait that gave up as well (umma_commit)
+            commits_done(&sm.pv_done, j);
+            for (int s = 0; s < 2; ++s) commits_done(&sm.s_full[s], (i + 1 - s) / 2);
+            for (int s = 0; s < kStages; ++s) commits_done(&sm.empty[s], (j + kStages - 1 - s) / kStages);
         }
         __syncwarp();
     } else {

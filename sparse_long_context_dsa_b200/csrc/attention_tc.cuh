@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *o_done = s_full + 8;
     uint64_t *x_full = o_done + 2;                        // [4 quarters][2 buffers]
     uint64_t *q_ready = x_full + 8;
-    uint64_t *mma_drain = q_ready + 1;                    // the MMA issuer's last commit
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_drain + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_ready + 1);
     static_assert((4 * kStages + 20) * 8 + 4 <= 512, "barriers fit their slot");
     float *xch = reinterpret_cast<float *>(smem + kOffXch);
     __shared__ uint32_t scan_ws[40];
@@ -345,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&o_done[1], 1);
         for (int b = 0; b < 8; ++b) mbar_init(&x_full[b], 2);
         mbar_init(q_ready, 8);
-        mbar_init(mma_drain, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
@@ -392,14 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&full[s], (last / kStages) & 1);
             }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (one lane): S(i), then O += P(i-2) V(i-2): S runs two tiles
+        // ---------------- MMA issuer (one elected lane): S(i), then O += P(i-2) V(i-2): S runs two tiles
         // ahead, so that the tensor pipe has S(i) queued while the softmax of tile i-1 runs
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(128, 64, false), kIdO = idesc_bf16(128, kD, true);
             // K: K-major, 8-token atoms 3 KiB apart; V: MN-major, 64-dim blocks 1 KiB apart
             const uint32_t k_lo0 = desc_lo(smem_u32(ks), 16), v_lo0 = desc_lo(smem_u32(vs), 1024);
             constexpr uint32_t kHi = desc_hi(kRegionBox);
             ok = mbar_wait(q_ready, 0);                   // Q in TMEM
+            int n_s = 0, n_pv = 0;                        // tiles whose S, whose P V went out
             auto issue_pv = [&](int j) {
                 const int s = j % kStages, pb = j & 1;
                 ok = ok && mbar_wait(&p_full[pb], (j >> 1) & 1) &&
@@ -417,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(&p_free[pb]);                       // P(j) read
                 umma_commit(&v_empty[s]);                       // V(j) read
                 umma_commit(&o_done[j & 1]);                    // O holds the tiles up to j
+                n_pv = j + 1;
             };
             for (int i = 0; i < n_tiles + 2 && ok; ++i) {
                 if (i >= n_tiles) {                             // the last two P V
@@ -436,12 +436,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_ts<true>(sd, tmem + kQCol + kk * 8, klo + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kHi, kIdS);
                 umma_commit(&s_full[sb]);
                 umma_commit(&k_empty[s]);                       // K(i) read
+                n_s = i + 1;
                 if (i >= 2) issue_pv(i - 2);
             }
-            // drain: no MMA of this CTA is in flight when TMEM is released, after a wait that
-            // gave up as well
-            umma_commit(mma_drain);
-            mbar_wait(mma_drain, 0);
+            // every commit has arrived when TMEM is released, after a wait that gave up as well
+            for (int b = 0; b < 2; ++b) {
+                commits_done(&o_done[b], (n_pv + 1 - b) / 2);
+                commits_done(&p_free[b], (n_pv + 1 - b) / 2);
+                commits_done(&s_full[b], (n_s + 1 - b) / 2);
+            }
+            for (int s = 0; s < kStages; ++s) {
+                commits_done(&v_empty[s], (n_pv + kStages - 1 - s) / kStages);
+                commits_done(&k_empty[s], (n_s + kStages - 1 - s) / kStages);
+            }
         }
     } else if (warp >= 4) {
         // ---------------- softmax warps 4..11: TMEM lane quarter warp % 4 (row r = query, head),

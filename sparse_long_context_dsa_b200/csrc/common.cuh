@@ -270,12 +270,35 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// True in one lane of a whole warp.
+__device__ __forceinline__ bool elect_one()
+{
+    unsigned one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // The mbarrier receives one arrival when all tcgen05 operations this thread issued so far
-// have completed.
+// have completed.  Every commit stands directly behind the MMAs it covers, issued by the same
+// elected lane: a commit on its own (a "drain" before the end of the kernel, on the heels of the
+// last tile's commits) was the last thing that a warp of a kernel that never ended had in hand, and
+// no bounded wait ends an instruction that does not complete.  The issuer waits for its last
+// commits instead (commits_done).
 __device__ __forceinline__ void umma_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
+}
+
+// Waits for the last of the n commits to `bar` (a phase each; 0: none): no MMA of theirs is in
+// flight, and no arrival is on its way, when TMEM and the barriers go.
+__device__ __forceinline__ void commits_done(uint64_t *bar, int64_t n)
+{
+    if (n > 0) mbar_wait(bar, (unsigned)(n - 1) & 1u);
 }
 
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per lane).

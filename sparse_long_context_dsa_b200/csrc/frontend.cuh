@@ -81,8 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(inv_freq + 32);
     uint64_t *full = bars, *empty = bars + kStages;                           // [kStages]
     uint64_t *acc_full = bars + 2 * kStages, *acc_empty = acc_full + 2;      // [2]
-    uint64_t *mma_drain = acc_empty + 2;                                     // the MMA issuer's last commit
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_drain + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -94,7 +93,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
         }
-        mbar_init(mma_drain, 1);
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < kDI; i += kThreads) {
@@ -136,9 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (one lane)
-        if (lane == 0) {
-            int it = 0, ui = 0;
+        // ---------------- MMA issuer (one elected lane)
+        if (elect_one()) {
+            int it = 0, ui = 0, units = 0;                    // it, units: stages and units committed
             for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x, ++ui) {
                 const int buf = ui & 1;
                 ok = mbar_wait_sleep(&acc_empty[buf], ((ui >> 1) & 1) ^ 1);
@@ -159,10 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 umma_commit(&acc_full[buf]);                      // the unit's accumulator is ready
+                ++units;
             }
-            // drain: no MMA of this CTA is in flight when TMEM is released
-            umma_commit(mma_drain);
-            mbar_wait(mma_drain, 0);
+            // every commit has arrived when TMEM is released, after a wait that gave up as well
+            for (int b = 0; b < 2; ++b) commits_done(&acc_full[b], (units + 1 - b) / 2);
+            for (int s = 0; s < kStages; ++s) commits_done(&empty[s], (it + kStages - 1 - s) / kStages);
         }
     } else {
         // ---------------- epilogue: warps 2..5; TMEM lane quarter sp = warp % 4 (the hardware's

@@ -216,9 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = bars + 2, *s_empty = bars + 2 + kSStages;                // [kSStages]
     uint64_t *acc_full = bars + 2 + 2 * kSStages, *acc_empty = acc_full + 2;    // [2]
     uint64_t *sc_empty = acc_empty + 2;                                         // [kSStages]
-    uint64_t *mma_drain = sc_empty + kSStages;                                  // the MMA issuer's last commit
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_drain + 1);
-    static_assert((2 + 3 * kSStages + 4 + 1) * 8 + 4 <= 256, "barriers fit their slot");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + kSStages);
+    static_assert((2 + 3 * kSStages + 4) * 8 + 4 <= 256, "barriers fit their slot");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -233,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], kEpiWarps);
         }
-        mbar_init(mma_drain, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
@@ -293,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (one lane)
-        if (lane == 0 && n_items > 0) {
+        // ---------------- MMA issuer (one elected lane)
+        if (n_items > 0 && elect_one()) {
             Walk w;
             walk_seek(p, lo, w);
             int cur_g = -1, cur_t = -1, q_loads = 0;
-            for (int64_t it = 0; it < n_items; ++it, walk_next(p, w)) {
+            int64_t it = 0, q_frees = 0;
+            for (; it < n_items; ++it, walk_next(p, w)) {
                 if (w.g != cur_g || w.t != cur_t) {
-                    if (q_loads > 0) umma_commit(q_empty);   // the old query tile is free once its MMAs finish
                     ok = mbar_wait_sleep(q_full, q_loads & 1);
                     if (!ok) break;
                     ++q_loads;
@@ -323,10 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 umma_commit(&s_empty[s]);            // the summary block may be overwritten
                 umma_commit(&acc_full[buf]);         // the accumulator is ready
+                if (w.rb + 1 == w.nb && it + 1 < n_items) {
+                    umma_commit(q_empty);            // the tile's last block: the next one's queries may land
+                    ++q_frees;
+                }
             }
-            // drain: no MMA of this CTA is in flight when TMEM is released
-            umma_commit(mma_drain);
-            mbar_wait(mma_drain, 0);
+            // every commit has arrived when TMEM is released, after a wait that gave up as well
+            for (int b = 0; b < 2; ++b) commits_done(&acc_full[b], (it + 1 - b) / 2);
+            for (int s = 0; s < kSStages; ++s) commits_done(&s_empty[s], (it + kSStages - 1 - s) / kSStages);
+            commits_done(q_empty, q_frees);
         }
     } else {
         // ---------------- epilogue: warps 2..9.  TMEM lane quarter sp = warp % 4 (the
