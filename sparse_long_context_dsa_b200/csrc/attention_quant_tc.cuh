@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float2 q2 = *reinterpret_cast<const float2 *>(&sm.qscale[2 * h]);
                     const float2 y = ffma2(make_float2(xs[16 + 2 * h], xs[17 + 2 * h]), make_float2(0.0625f, 0.0625f),
                                            make_float2(xs[2 * h], xs[2 * h + 1]));
-                    s[h] = fmul2(fmul2(y, ks2), q2);
+                    s[h] = fmul2(y, fmul2(ks2, q2));             // (the scales first: y times one of them may overflow)
                 }
                 if (!all_ok) {
 #pragma unroll
