@@ -500,15 +500,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&sm.merged, (unsigned)n_run & 1u);
             __syncwarp();
             tc_fence_after();
-            float w[2] = {0.0f, 0.0f};                           // of each group's O
+            float w[2] = {0.0f, 0.0f}, e2;                       // of each group's O, then of their sum
             {
                 const float4 a = sm.merge[0][row], b = sm.merge[1][row];
                 m = fmaxf(a.x, b.x);
                 M = fmaxf(a.y, b.y);
                 // (a sum without a reference is 0 or NaN)
                 l = (a.x == -INFINITY ? a.z : a.z * exp2f(a.x - m)) + (b.x == -INFINITY ? b.z : b.z * exp2f(b.x - m));
-                // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
-                const float f = l > 0.0f ? (M > -INFINITY ? exp2f(M - m) / l : 0.0f) : l;
+                // 1 / l, then 2^(M - m) (their product may be below fp32's range); 0 for a row with no token or no
+                // V; a NaN sum stays NaN (no comparison holds for it)
+                const float f = l > 0.0f ? 1.0f / l : l;
+                e2 = M > -INFINITY ? exp2f(M - m) : 0.0f;
                 w[0] = a.y == -INFINITY ? 0.0f : exp2f(a.y - M);
                 w[1] = b.y == -INFINITY ? 0.0f : exp2f(b.y - M);
                 w[0] *= f;
@@ -534,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4 *>(rows + lane * kD + (((c0 / 8 + i) ^ ((lane >> 1) & 3)) << 4)) =
-                        make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                   pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                        make_uint4(pack_bf16x2(o[8 * i] * e2, o[8 * i + 1] * e2), pack_bf16x2(o[8 * i + 2] * e2, o[8 * i + 3] * e2),
+                                   pack_bf16x2(o[8 * i + 4] * e2, o[8 * i + 5] * e2),
+                                   pack_bf16x2(o[8 * i + 6] * e2, o[8 * i + 7] * e2));
             }
             __syncwarp();
             // (out is 8-byte aligned: two stores of 8 bytes where it is not 16-byte aligned)

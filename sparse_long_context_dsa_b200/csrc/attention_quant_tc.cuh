@@ -604,8 +604,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (warp == 0 && lane < 16) {
                 const float L = (sm.red[0][lane] + sm.red[1][lane]) + (sm.red[2][lane] + sm.red[3][lane]);
                 const float m = sm.m[lane], M = sm.M[lane];
-                // 0 for a row with no token or no V; a NaN sum stays NaN (no comparison holds for it)
-                sm.f[lane] = S > 1 ? L : L > 0.0f ? (M > -INFINITY ? exp2f(M - m) / L : 0.0f) : L;
+                // O times 1 / L, then 2^(M - m) (their product may be below fp32's range); 0 for a row with no
+                // token or no V; a NaN sum stays NaN (no comparison holds for it)
+                sm.f[lane] = S > 1 ? L : L > 0.0f ? 1.0f / L : L;
+                sm.ao[lane] = M > -INFINITY ? exp2f(M - m) : 0.0f;
                 if (S == 1 && p.lse) p.lse[head0 + lane] = L == 0.0f ? -INFINITY : (m - kBase + log2f(L)) * 0.69314718055994531f;
             }
             if (x.n_tiles > 0) wait(&sm.pv_done, (unsigned)(tg - 1) & 1u);
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int d = 64 * h2 + 32 * warp + lane;
 #pragma unroll
                 for (int h = 0; h < 16; ++h) {
-                    if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h]);
+                    if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h] * sm.ao[h]);
                     else stage[h * kInRow + d] = o[h];
                 }
             }
@@ -684,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             x += wt * v.x;
             y += wt * v.y;
         }
-        const float f = Ls > 0.0f ? (MM > -INFINITY ? exp2f(MM - mm) / Ls : 0.0f) : Ls;
+        const float f = Ls > 0.0f ? 1.0f / Ls : Ls, e2 = MM > -INFINITY ? exp2f(MM - mm) : 0.0f;
         const int64_t head = head0 + rank + S * j;
-        *reinterpret_cast<uint32_t *>(p.out + head * kD + d) = pack_bf16x2(x * f, y * f);
+        *reinterpret_cast<uint32_t *>(p.out + head * kD + d) = pack_bf16x2(x * f * e2, y * f * e2);
         if (p.lse && d == 0) p.lse[head] = Ls == 0.0f ? -INFINITY : (mm - kBase + log2f(Ls)) * 0.69314718055994531f;
     }
     // this CTA's copies have read their rows before its shared memory goes away

@@ -45,3 +45,29 @@ def test_scales_whose_product_is_ordinary(n, up, down):
     Q.check_attention(out, lse, Q.attention(qd, cache.numpy(), scale.numpy(), table, [0] * n, pos, Q.sel_tokens(sel, cnt, pos)))
     out, lse = attend(cache, scale, table, q, pos, w=200)
     Q.check_attention(out, lse, Q.attention(qd, cache.numpy(), scale.numpy(), table, [0] * n, pos, Q.window_tokens(pos, 200)))
+
+
+def whole(n, pos):
+    """Selections of every region up to the query's own."""
+    sel = np.tile(np.arange(pos // 8 + 1, dtype=np.int32), (n, 4, 1))
+    return sel, np.full((n, 4), pos // 8 + 1, np.int32)
+
+
+@pytest.mark.parametrize("n", [1, 75])
+@pytest.mark.parametrize("kind", ["selection", "window"])
+def test_smallest_values_over_many_tokens(kind, n):
+    # 15,887 tokens of equal weight, values at the smallest scale and of one sign: the weights' sum times
+    # 2^126 passes the numbers' range, the outputs (some 2^-119) do not
+    L = 15887
+    pages = (L + 63) // 64
+    table = Q.random_table([L], pages, 5)
+    cache, scale = Q.filled_cache(pages, 6, 0.0)
+    cache &= 0x7F
+    scale[..., 1] = 2.0 ** -126
+    q = torch.zeros((n, 64, 192), dtype=torch.bfloat16)
+    pos = [L - 1] * n
+    sel, cnt = whole(n, L - 1)
+    out, lse = attend(cache, scale, table, q, pos, w=L) if kind == "window" else attend(cache, scale, table, q, pos, sel=sel, cnt=cnt)
+    ref = Q.attention(q[:1].double().numpy(), cache.numpy(), scale.numpy(), table, [0], pos[:1], Q.sel_tokens(sel, cnt, pos))
+    Q.check_attention(out[:1], lse[:1], ref)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
