@@ -378,7 +378,8 @@ dsa_status_t dsa_sparse_attn_decode_groups(const void *q, const void *k_cache, c
  * q_pos[i] % 64 of page block_table[b*max_pages + q_pos[i]/64], b = q_req[i] (q_req NULL: b = i).
  * A block's scale is the smallest power of two s in [2^-126, 2^120] with max|x| <= 448 s (0 for
  * zeros), a code is e4m3_RNE_satfinite(x / s).  Neighbouring list entries in one region of one
- * request are a run and have ascending positions; a region has at most one run per call.  Below
+ * request are a run and have ascending positions; a region of a page has at most one run per call
+ * (a list ordered step by step over its requests has more; so has a chunk that laps a ring).  Below
  * the first row of its run a block keeps its rows: its scale becomes the larger of the old one
  * and the run's, and codes of a smaller scale are rounded again for it (exact for powers of two,
  * but for e4m3 subnormals).  Rows behind the run keep their bytes, but not their values where the
@@ -387,7 +388,8 @@ dsa_status_t dsa_sparse_attn_decode_groups(const void *q, const void *k_cache, c
  * take their block's scale to 2^120; NaN stays NaN and leaves the scale to the other values.  A
  * q_req outside [0, n_req), a position that is negative or beyond the block table, a page
  * outside [0, n_pages), and in a run an entry that does not ascend with those behind it, are skipped
- * and flag DSA_ERR_DEVICE. */
+ * and flag DSA_ERR_DEVICE.  With q_req a region in two runs flags it too; what that region then
+ * holds is unspecified. */
 dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_pages, const int32_t *block_table,
                                  int max_pages, int n_req, const int32_t *q_req, const int32_t *q_pos, int n,
                                  const void *new_k, const void *new_v, dsa_stream_t stream);

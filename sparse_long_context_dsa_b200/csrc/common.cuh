@@ -29,6 +29,7 @@ enum : unsigned {
     kErrTopkInternal = 1u << 5,    // selection bookkeeping inconsistent
     kErrAppendOrder = 1u << 6,     // quantised append: a region's rows not in ascending order
     kErrPages = 1u << 7,           // page fork / release / compact: an index, a count or no free page
+    kErrAppendTwice = 1u << 8,     // quantised append: a region of a page in two runs of a call
 };
 
 __device__ unsigned int g_error_word;

@@ -710,6 +710,7 @@ dsa_status_t dsa_check_device(dsa_stream_t stream)
     if (word & dsa::kErrWaitTimeout) msg += " bounded wait timed out;";
     if (word & dsa::kErrTopkInternal) msg += " top-k internal inconsistency;";
     if (word & dsa::kErrAppendOrder) msg += " quantised append: positions of a region not ascending;";
+    if (word & dsa::kErrAppendTwice) msg += " quantised append: a region of a page in two runs of a call;";
     if (word & dsa::kErrPages) msg += " pages: index or count out of range, or no free page;";
     return fail(DSA_ERR_DEVICE, msg);
 }
@@ -1330,12 +1331,14 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
     // hold no run's first.  us with 1 / 8: a chunk of 64 tokens 2.7 / 3.6, 512 3.6 / 3.7, 1,024 4.6 / 4.0,
     // 2,048 5.9 / 4.1; a decode step's runs are single tokens, and 8 of them in one CTA wait for one
     // another: 8 requests 2.7 / 10.4, 1,024 7.5 / 13.3, 4,096 27.5 / 30.6.
+    const unsigned looks = q_req ? (unsigned)(((int64_t)n + dsa::quant::kSeenEntries - 1) / dsa::quant::kSeenEntries) : 0u;
+    const dim3 threads(dsa::quant::kThreads);
     if (!q_req || n < 8 * (int64_t)n_req || n <= 4 * sms)
-        return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<1>, dim3((unsigned)n), dim3(256), 0,
-                        stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n, nk, nv);
-    return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<8>, dim3((unsigned)((n + 7) / 8)),
-                    dim3(256), 0, stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n,
-                    nk, nv);
+        return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<1>, dim3((unsigned)n + looks), threads, 0,
+                        stream, 0, kv_cache, kv_scale, n_pages, block_table, max_pages, q_req, rows, q_pos, n, nk, nv, looks);
+    return launch_k("kv_append_quant_kernel", dsa::quant::kv_append_quant_kernel<8>,
+                    dim3((unsigned)(((int64_t)n + 7) / 8) + looks), threads, 0, stream, 0, kv_cache, kv_scale, n_pages,
+                    block_table, max_pages, q_req, rows, q_pos, n, nk, nv, looks);
 }
 
 dsa_status_t dsa_sparse_attn_decode_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,

@@ -536,7 +536,7 @@ def quant_cache(n_pages, device="cuda"):
 def kv_append_quant(kv_cache, kv_scale, block_table, q_pos, new_k, new_v, q_req=None):
     """dsa_kv_append_quant: token i's K and V rows (new_k, new_v bf16 [n][4][192]) quantised into the
     8-bit cache at position q_pos[i] of request q_req[i] (or i).  Tokens of one region are
-    neighbours in the list, in ascending order."""
+    neighbours in the list, in ascending order; a region that comes up again is flagged."""
     st = _native().kv_append_quant(kv_cache, kv_scale, block_table, q_pos, new_k, new_v, q_req)
     if st < 0:
         _quant_cache_args(kv_cache, kv_scale, block_table)
