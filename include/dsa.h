@@ -434,7 +434,12 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
  *   before it that copy one.  Other entries of the row become -1 (whatever it held is not
  *   released).  A child is no fork's parent and no other fork's child in the same call.
  * dsa_pages_release: row req[i] is cut to its first keep[i] tokens (0: all given back): pages
- *   behind them lose this holder, their entries become -1.
+ *   behind them lose this holder, their entries become -1.  A cut that ends inside a page keeps
+ *   that page, shared or not: where others hold it too, an append from token keep[i] on would
+ *   write into their tokens (and may raise their blocks' scales), and no append looks at counts.
+ *   Such a row is attended as it is, but before it is appended to, a fork of its first keep[i]
+ *   tokens into a free row gives it a copy of that page, and a release of the old row (keep 0)
+ *   returns what it held.
  * dsa_pages_compact: the n_live live pages move to the places 0 .. n_live - 1: those behind, from
  *   the last one down, go to the free places among them, from the first one up.  new_index int32
  *   [n_pages]: the new place of every page, -1 for a free one; n_live int32 [1].  The table, the

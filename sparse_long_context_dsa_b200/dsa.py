@@ -635,6 +635,8 @@ def pages_fork(ref, block_table, parent, child, length, pools, ref_out=None, tab
 
 def pages_release(ref, block_table, req, keep, ref_out=None, table_out=None):
     """dsa_pages_release: rows req[i] cut to their first keep[i] tokens, the pages behind given back.
+    A row cut inside a page that others hold too is not appended to: pages_fork of its first keep[i]
+    tokens into a free row copies that page, a release of the old row gives it back.
     In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
     ref_out = ref if ref_out is None else ref_out
     table_out = block_table if table_out is None else table_out
