@@ -426,7 +426,11 @@ dsa_status_t dsa_window_attn_quant(const void *q, const uint8_t *kv_cache, const
  * takes the lowest free pages, so results are functions of the arguments alone.  n <= 4096,
  * max_pages < 2^31 / 64.  A pool is an array [n_pages] of pages of page_bytes (a multiple of 16,
  * 16-byte aligned): the caches of every layer that share a block table, with their scales.
- * `pools` is a host array, read during the call.
+ * `pools` is a host array of at most DSA_MAX_PAGE_POOLS, read during the call; more pools take more
+ * calls, from the same inputs into outputs of their own, which then agree (in place the second call
+ * would find the first one's result).
+ * What a runtime does itself, between calls: to give a request its next page when its tokens
+ * reach a page's end, with a count of 1 (ahead of time, or the lowest page whose count is 0).
  *
  * dsa_pages_fork: for i = 0 .. n - 1, row child[i] becomes a request of the first length[i] tokens
  *   of row parent[i]: it shares the full pages (their counts rise) and, for a partly filled last

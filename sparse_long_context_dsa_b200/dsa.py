@@ -621,7 +621,8 @@ def pages_fork(ref, block_table, parent, child, length, pools, ref_out=None, tab
     """dsa_pages_fork: rows child[i] of block_table [n_req][max_pages] become requests of the first
     length[i] tokens of rows parent[i]: full pages shared (ref int32 [n_pages] counts holders), a
     partly filled last one copied to the lowest free page in every pool (a list of [n_pages][...]
-    tensors).  In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
+    tensors, at most MAX_PAGE_POOLS: more take more calls, each with ref_out and table_out of its own).
+    In place unless ref_out / table_out are given.  Returns (ref_out, table_out)."""
     ref_out = ref if ref_out is None else ref_out
     table_out = block_table if table_out is None else table_out
     st = _native().pages_fork(ref, block_table, parent, child, length, pools, ref_out, table_out)
