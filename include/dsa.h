@@ -397,11 +397,17 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
 /* dsa_sparse_attn_decode_quant, dsa_sparse_attn_prefill_quant, dsa_window_attn_quant: the attention
  * of dsa_sparse_attn_decode, dsa_sparse_attn_prefill and dsa_window_attn over this cache, with
  * their arguments, results and errors (nq <= 2^24, out 8-byte aligned; a query at a negative
- * position attends nothing: out = 0, lse = -inf).  Scales are finite and >= 0, powers of two or not.
- * Scores and sums are fp32; q enters the products as two e4m3 terms (off by at most 2^-18 of the
- * head's largest element; infinities saturate), the softmax weights as fp16.  Tokens outside a query's T may hold any
- * bytes, NaN codes among them.  The results do not depend on the other queries of the call.  No
- * workspace. */
+ * position attends nothing: out = 0, lse = -inf).  Scales are 0 or normal fp32 numbers, powers of two or not.
+ * Scores and sums are fp32.  q enters the products as two e4m3 terms, off by at most 2^-21 of the
+ * head's largest element, 2^-17 in a window call that names requests (both of at least 2^-118;
+ * infinities saturate); a softmax weight, times V's scale, as fp16 cut into three e5m2 terms: off by
+ * at most 2^-9 + 2^-11 of itself and 2^-22 of its head's largest.  Tokens outside a query's T may
+ * hold any bytes, NaN codes among them.  A query's result depends on the other queries of the call
+ * in its rounding alone (how a row is split and which kernel takes a window follow the number of
+ * queries, the neighbours in the list and the number of rows of the block table); the same call gives
+ * the same bits.  A list of q_req that takes several queries of each request goes best with a block
+ * table of the call's requests only: window calls share the loads of neighbouring queries, and appends
+ * take 8 tokens at a time, from 8 list entries per row of the table on.  No workspace. */
 dsa_status_t dsa_sparse_attn_decode_quant(const void *q, const uint8_t *kv_cache, const float *kv_scale,
                                           int64_t n_pages, const int32_t *block_table, int max_pages,
                                           const int32_t *q_pos, int batch, const int32_t *sel_idx,

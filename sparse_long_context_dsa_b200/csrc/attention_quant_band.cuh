@@ -6,8 +6,9 @@
 // one stream of their windows' pages (64 tokens, 24 KiB, a ring of 4); rows of the
 // other runs are masked.  A prefill chunk's 8 queries are one run.
 //  * S = q K^T: tcgen05.mma kind::f8f6f4 straight from the codes (K-major, 64-byte swizzle), q as
-//    two e4m3 terms of 2^-e q that accumulate into the same S (the second is off by at most 2^-18
-//    of the head's largest element);
+//    two e4m3 terms of 2^-e q that accumulate into the same S.  The largest of 2^-e q is above 224
+//    and the terms end at the subnormal step 2^-9, so q is off by at most 2^-10 / 224 < 2^-17 of the
+//    head's largest element (the row kernel's second term, 16 times finer, needs a product of its own);
 //  * softmax: thread = row (TMEM lane), fp32, log2 units, no exchange between threads.  As in the
 //    row kernel, the sum l has a reference m and the weights P' = 2^(s - m) sV 2^(m - M) one of
 //    their own, both moved only when a tile passes them by 2^10 (O is then rescaled in TMEM);

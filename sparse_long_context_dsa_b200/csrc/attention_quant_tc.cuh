@@ -6,8 +6,8 @@
 // and V's 8 rows as the MMAs take them).  tokens (S) and dims (O) are the MMA's M, the 16 heads
 // its N: a row has no more of them.
 //  * S^T = K q^T: kind::f8f6f4 straight from the codes, 6 steps of K = 32.  2^-e q = hi + lo / 16 in
-//    e4m3 side by side in N (off by at most 2^-18 of the head's largest element); the codes' scale
-//    and q's multiply the fp32 sums.
+//    e4m3 side by side in N (off by at most 2^-14 / 224 < 2^-21 of the head's largest element, which is
+//    above 224 there); the codes' scale and q's multiply the fp32 sums.
 //  * softmax: thread = token, fp32, log2 units, against references m (of s) and M (of s + log2 of V's
 //    scale) of each head that move only where a weight passes 2^15 (then O is rescaled in TMEM).
 //  * O^T += V^T P'^T: V's codes MN-major, P' = 2^(s - m) sV 2^(m - M) as three e5m2 terms (cut off, cut

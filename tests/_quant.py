@@ -75,12 +75,13 @@ def append(cache, scale, table, req, pos, new_k, new_v):
     return cache, scale
 
 
-def attention(q, cache, scale, table, req, pos, tokens):
+def attention(q, cache, scale, table, req, pos, tokens, q_off=2.0 ** -18):
     """Rows of 64-bit attention and the tolerances of the GPU's.  q float64 [nq][64][192]; tokens(i, g):
     positions attended by row (i, g).  Returns out, lse [nq][64], and out_tol, lse_tol.
 
-    The tolerances count, per head: the score's error d (q as two e4m3 terms, the second 16 times
-    finer: off by at most 2^-18 of the head's largest element; 192 fp32 sums; the scaled score and exp2's
+    The tolerances count, per head: the score's error d (q as two e4m3 terms: off by at most q_off of the
+    head's largest element, 2^-21 where the second term is 16 times finer and 2^-17 where it is not,
+    as test_gpu_quant_bounds.py derives and checks; 192 fp32 sums; the scaled score and exp2's
     argument rounded), a weight's relative error 2 d (its own and the sum's), its rounding to fp16
     (2^-11) and from there to three e5m2 terms (of a weight in [1, 2) the first, cut off, leaves less
     than 2^-2, the second of that less than 2^-5, the third, rounded, at most 2^-9; all three end at the
@@ -109,7 +110,7 @@ def attention(q, cache, scale, table, req, pos, tokens):
             out[i, h] = w @ v
             lse[i, h] = (m + np.log(z))[:, 0]
             absqk = np.abs(qq) @ np.abs(k).T / math.sqrt(D)
-            d = (2.0 ** -18 * np.abs(qq).max(1)[:, None] * np.abs(k).sum(1)[None] / math.sqrt(D) +
+            d = (q_off * np.abs(qq).max(1)[:, None] * np.abs(k).sum(1)[None] / math.sqrt(D) +
                  192 * 2.0 ** -24 * absqk).max(1) + 2.0 ** -20 * (np.abs(s).max(1) + 1)
             ws = w * sc[:, 1]                                     # weights of the codes
             rounding = (2.0 ** -9 + 2.0 ** -11) * ws + 2.0 ** -22 * ws.max(1, keepdims=True)
