@@ -631,10 +631,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
                 }
                 const int d = 64 * h2 + 32 * warp + lane;
+                if (S == 1) {
 #pragma unroll
-                for (int h = 0; h < 16; ++h) {
-                    if (S == 1) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h] * sm.ao[h]);
-                    else stage[h * kInRow + d] = o[h];
+                    for (int h = 0; h < 16; ++h) p.out[(head0 + h) * kD + d] = __float2bfloat16_rn(o[h] * sm.f[h] * sm.ao[h]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) stage[h * kInRow + d] = o[h];
                 }
             }
             if (S > 1) {
