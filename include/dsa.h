@@ -383,8 +383,8 @@ dsa_status_t dsa_sparse_attn_decode_groups(const void *q, const void *k_cache, c
  * the first row of its run a block keeps its rows: its scale becomes the larger of the old one
  * and the run's, and codes of a smaller scale are rounded again for it (exact for powers of two,
  * but for e4m3 subnormals).  Rows behind the run keep their bytes, but not their values where the
- * scale changes: a ring therefore holds the window and a region more (9 pages for 512 tokens), and
- * a token is appended again after a rollback before it is attended.  Infinities saturate and
+ * scale changes: a ring therefore holds the window and a region more (9 pages for 512 tokens; the
+ * tokens of a chunk more where it is appended before its queries attend), and a token is appended again after a rollback before it is attended.  Infinities saturate and
  * take their block's scale to 2^120; NaN stays NaN and leaves the scale to the other values.  A
  * q_req outside [0, n_req), a position that is negative or beyond the block table, a page
  * outside [0, n_pages), and in a run an entry that does not ascend with those behind it, are skipped

@@ -17,12 +17,13 @@
 // Warps: 0-3 softmax, 4 loads (the lookups of the next 32 regions run ahead), 5 the MMAs' issuer.
 //
 // Bound: a row's chain load - S - softmax - P' V - the next weights, with two CTAs per SM and two tiles
-// each in flight: of ~3,000 cycles a tile the weights take 900 and the P' V behind them 1,000.  k = 512:
-// one decode at 16,384 tokens 10.1 us (latency: 64 CTAs of two tiles), 8 at 131,072 19.4 us (2.6 TB/s), 32 of
-// 4,096 .. 262,144 47.4 us (4.3 TB/s, 0.66 of the copy rate), a chunk of 256 queries at 32,768 210 us (1.6 GB
-// of gathers from L2, 7.7 TB/s; with the issuer as lane 0 in place of an elected lane 229: tensor pipe
-// 17 %, issue slots 36 %).  Tried and not faster (the chunk, us against those 229): regions as boxes of 128 and 64 dims, two rows of a
-// token in place of three 243; K's and V's places released apart 236; eight softmax warps of 8 heads 238.
+// each in flight: of ~3,000 cycles a tile the weights take 900 and the P' V behind them 1,000.  k = 512,
+// a call from Python (in a graph): one decode at 16,384 tokens 11.7 us (9.9; latency: 64 CTAs of two tiles;
+// the bf16 kernel, twice the bytes, 8.6), 8 at 131,072 19.3 us (17.0; 2.6 TB/s), 32 of 4,096 .. 262,144
+// 47.5 us (4.3 TB/s, 0.66 of the copy rate), a chunk of 256 queries at 32,768 212 us (184; 1.6 GB of gathers
+// from L2, 7.7 TB/s; tensor pipe 18 %, issue slots 39 %).  Tried and not faster (the chunk, us against 229 with the
+// issuer as lane 0 in place of an elected lane): regions as boxes of 128 and 64 dims, two rows of a token
+// in place of three 243; K's and V's places released apart 236; eight softmax warps of 8 heads 238.
 #pragma once
 
 #include <type_traits>

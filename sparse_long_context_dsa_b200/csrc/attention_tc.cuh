@@ -15,7 +15,7 @@
 //    [8 rows][128 B] with the 128-byte swizzle (8-token atoms 3 KiB apart), into separate
 //    4-stage rings: a K stage frees as soon as S has read it, a V stage once P V has; a region
 //    that is invalid or past the union is loaded from rows past the cache, which fill zeros;
-//  * one thread issues S = Q K^T (M = 128, N = 64, K = 192: 12 tcgen05.mma.kind::f16, Q
+//  * one elected thread issues S = Q K^T (M = 128, N = 64, K = 192: 12 tcgen05.mma.kind::f16, Q
 //    read from TMEM where the softmax warps put it at the start) into one of two 64-column
 //    TMEM buffers, and O += P V (M = 128, N = 192, K = 64: 4 MMAs with
 //    P read from TMEM and V an MN-major smem operand) into a 192-column TMEM accumulator;
@@ -28,7 +28,9 @@
 //    as packed bf16 into TMEM (two tokens per column, the A operand of P V), and at the end
 //    write O / l and the LSE.
 // Every wait is bounded; after the loops the producers wait for their last loads and the MMA
-// issuer for a final commit, so nothing is in flight when TMEM is released.
+// issuer for the last arrival on every barrier it committed to, so nothing is in flight when TMEM
+// is released.  2,048 queries on 262,144 tokens whose neighbours share selections: 0.49 ms (0.593 with
+// the issuer as lane 0 in place of an elected lane).
 // Blocks spanning several requests, with an invalid query, or whose union exceeds twice the
 // longest selection are flagged in row_shared and left to the per-row kernel that runs next.
 #pragma once

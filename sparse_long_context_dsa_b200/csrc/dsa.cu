@@ -1262,9 +1262,10 @@ dsa_status_t attn_quant_common(const void *q, const uint8_t *kv_cache, const flo
     p.k = k;
     p.window = window;
     p.scale_log2 = dsa::attnq::kLog2e / sqrtf((float)dsa::kD);
-    // Chunks: 8 neighbouring queries of the list share their windows' tokens, where a request has at
-    // least that many queries on average (a decode list's neighbours are different requests) and the
-    // rows are more than one round of CTAs (windows below 128: two).  Shared / row by row, us: 74
+    // Chunks: 8 neighbouring queries of the list share their windows' tokens, where the block table has
+    // at most one row for every 8 of them (a decode list's neighbours are different requests; the list
+    // itself is on the device, so a table of more rows than the call's requests counts against it) and
+    // the rows are more than one round of CTAs (windows below 128: two).  Shared / row by row, us: 74
     // queries 15.3 / 10.3 (window 128), 17.5 / 12.5 (256); 80 queries 22.2 / 27.3 (512), 31.3 / 35.3
     // (1,024); 128 queries 15.6 / 16.5 (128), 13.6 / 11.5 (64); 160 queries 13.9 / 15.7 (64).
     if (window > 0 && nq >= 8 * (int64_t)n_req && (int64_t)nq * dsa::kG > resident * (window < 128 ? 2 : 1)) {
@@ -1327,8 +1328,8 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
     if ((st = device_info(sms)) != DSA_OK) return st;
     const int rows = q_req ? n_req : n;
     const __nv_bfloat16 *nk = static_cast<const __nv_bfloat16 *>(new_k), *nv = static_cast<const __nv_bfloat16 *>(new_v);
-    // One list entry per CTA, or 8 (one run, as a rule) for long chunks, where most CTAs of one entry
-    // hold no run's first.  us with 1 / 8: a chunk of 64 tokens 2.7 / 3.6, 512 3.6 / 3.7, 1,024 4.6 / 4.0,
+    // One list entry per CTA, or 8 (one run, as a rule) for long chunks (8 entries for every row of the
+    // block table), where most CTAs of one entry hold no run's first.  us with 1 / 8: a chunk of 64 tokens 2.7 / 3.6, 512 3.6 / 3.7, 1,024 4.6 / 4.0,
     // 2,048 5.9 / 4.1; a decode step's runs are single tokens, and 8 of them in one CTA wait for one
     // another: 8 requests 2.7 / 10.4, 1,024 7.5 / 13.3, 4,096 27.5 / 30.6.
     const unsigned looks = q_req ? (unsigned)(((int64_t)n + dsa::quant::kSeenEntries - 1) / dsa::quant::kSeenEntries) : 0u;
