@@ -34,6 +34,11 @@ def torch_version():
     try:
         return metadata.version("torch")
     except metadata.PackageNotFoundError:
+        pass
+    try:                               # a torch without package metadata
+        import torch
+        return str(torch.__version__)
+    except ImportError:
         return None
 
 
