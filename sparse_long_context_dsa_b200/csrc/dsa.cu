@@ -1329,9 +1329,10 @@ dsa_status_t dsa_kv_append_quant(uint8_t *kv_cache, float *kv_scale, int64_t n_p
     const int rows = q_req ? n_req : n;
     const __nv_bfloat16 *nk = static_cast<const __nv_bfloat16 *>(new_k), *nv = static_cast<const __nv_bfloat16 *>(new_v);
     // One list entry per CTA, or 8 (one run, as a rule) for long chunks (8 entries for every row of the
-    // block table), where most CTAs of one entry hold no run's first.  us with 1 / 8: a chunk of 64 tokens 2.7 / 3.6, 512 3.6 / 3.7, 1,024 4.6 / 4.0,
-    // 2,048 5.9 / 4.1; a decode step's runs are single tokens, and 8 of them in one CTA wait for one
-    // another: 8 requests 2.7 / 10.4, 1,024 7.5 / 13.3, 4,096 27.5 / 30.6.
+    // block table), where most CTAs of one entry hold no run's first.  us with 1 / 8, calls in a graph: a chunk
+    // of 64 tokens 2.5 / 2.5, 512 3.6 / 2.8, 1,024 4.4 / 3.1, 2,048 5.8 / 3.7, 8,192 14.7 / 10.3; a decode step's
+    // runs are single tokens, and 8 of them in one CTA wait for one another: 8 requests 2.7 / 10.7, 1,024
+    // 7.2 / 13.2, 4,096 23.5 / 25.1.
     const unsigned looks = q_req ? (unsigned)(((int64_t)n + dsa::quant::kSeenEntries - 1) / dsa::quant::kSeenEntries) : 0u;
     const dim3 threads(dsa::quant::kThreads);
     if (!q_req || n < 8 * (int64_t)n_req || n <= 4 * sms)
